@@ -494,6 +494,121 @@ w4_status awq_clip_search(const uint16_t* X, int64_t T, const uint16_t* W, int64
                           void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Feed-forward operators on quantised layers.
+ *
+ * The library's linear layers with what surrounds them in a feed-forward block: the epilogue of a
+ * matmul (bias, activation, residual), the gated pair of projections, and the input gradients that
+ * training through frozen quantised weights needs (adapters, biases and norms learn; the INT4
+ * weights do not).  A gated block's forward pass is w4_gemm_gated then w4_gemm_fused with the
+ * residual; its backward pass is w4_gemm_dx_gated (down projection and gate) then w4_gemm_dx (gate
+ * and up projections).  The pages have no counterpart to these calls.
+ *
+ * Conventions, beside the ones above: W = dequant(packed, scales, zeros) [N, K] = (q - z) s exactly;
+ * products accumulate in fp32 and everything up to an output's one rounding to fp16 stays in fp32
+ * (exceptions are stated at the call).  scales and zeros need no alignment; every other array is
+ * 16-byte aligned, ws included.  An optional array is absent when its pointer is NULL.  Outputs
+ * must not overlap inputs except where the call says so.  M, N or K may be zero: an empty sum is 0.
+ * N % 8 == 0, K % 128 == 0, group 128.  Calls on the same stream may share a workspace; calls that
+ * may overlap on the GPU (other streams, two graphs replayed together) need one each.
+ */
+typedef enum {
+    W4_ACT_NONE = 0,
+    W4_ACT_RELU = 1,      /* max(x, 0); derivative 0 at 0 */
+    W4_ACT_GELU = 2,      /* x Phi(x), Phi the normal distribution function */
+    W4_ACT_GELU_TANH = 3, /* x / 2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+    W4_ACT_SILU = 4       /* x / (1 + exp(-x)) */
+} w4_activation;
+
+/* Bytes of device workspace w4_gemm_fused needs for this shape (may be 0). */
+w4_status w4_gemm_fused_workspace_size(int64_t M, int64_t N, int64_t K, int group, size_t* bytes);
+
+/*
+ * w4_gemm_fused -- Y = act(X . W^T + bias) + residual, one rounding to fp16.
+ *
+ *   X [M, K] fp16; bias [N] fp16 or NULL; residual [M, N] fp16 or NULL (may be Y itself: added in
+ *   place); Y [M, N] fp16 out; Z [M, N] fp16 out or NULL: X . W^T + bias, which w4_act_backward
+ *   takes.
+ *   flags: 0 or W4_FLAG_WEIGHTS_STATIC (see w4_variant; covers packed, scales and zeros).
+ *   Backward pass: w4_act_backward (dZ, dbias; skip it without activation and bias), w4_gemm_dx;
+ *   the residual's gradient is dY.
+ * Errors: W4_ERR_UNSUPPORTED for an unknown activation or flag; else as w4_gemm.
+ */
+w4_status w4_gemm_fused(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
+                        const uint16_t* scales, const uint8_t* zeros, int group, const uint16_t* bias,
+                        int activation, const uint16_t* residual, uint16_t* Y, uint16_t* Z, void* ws,
+                        size_t ws_bytes, int flags, void* stream);
+
+/* Bytes of device workspace w4_gemm_gated needs for this shape (may be 0). */
+w4_status w4_gemm_gated_workspace_size(int64_t M, int64_t N, int64_t K, int group, size_t* bytes);
+
+/*
+ * w4_gemm_gated -- H = act(X . Wg^T) * (X . Wu^T): both projections of a gated feed-forward block,
+ * the activation and the product in one pass over X and the weights.
+ *
+ *   X [M, K] fp16; gate and up projection: two layers of the same shape [N, K]; H [M, N] fp16 out.
+ *   G, U [M, N] fp16 out, both or neither (NULL): X . Wg^T and X . Wu^T, which the backward pass
+ *   takes.  H is formed from the fp32 sums, not from the rounded G and U.
+ *   flags: 0 or W4_FLAG_WEIGHTS_STATIC.
+ * Errors: as w4_gemm_fused; W4_ERR_NULL when only one of G and U is given.
+ */
+w4_status w4_gemm_gated(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* gate_packed,
+                        const uint16_t* gate_scales, const uint8_t* gate_zeros, const uint32_t* up_packed,
+                        const uint16_t* up_scales, const uint8_t* up_zeros, int group, int activation,
+                        uint16_t* H, uint16_t* G, uint16_t* U, void* ws, size_t ws_bytes, int flags,
+                        void* stream);
+
+/* Bytes of device workspace w4_gemm_dx (n_layers 1 or 2) or w4_gemm_dx_gated (n_layers 1) needs
+ * (may be 0).  Other n_layers: W4_ERR_UNSUPPORTED. */
+w4_status w4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int n_layers, int group, size_t* bytes);
+
+/*
+ * w4_gemm_dx -- dX = dY . W, or dX = dY . W + dY2 . W2: the input gradient of one quantised layer,
+ * or of two layers of the same shape that share their input (gate and up projection).
+ *
+ *   dY, dY2 [M, N] fp16; W, W2 [N, K] (quantised along K as everywhere); dX [M, K] fp16 out.  One
+ *   layer: dY2, packed2, scales2 and zeros2 all NULL; two layers: none of them.
+ * Errors: as w4_gemm; W4_ERR_NULL when the second layer is given in part.
+ */
+w4_status w4_gemm_dx(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
+                     const uint16_t* scales, const uint8_t* zeros, const uint16_t* dY2,
+                     const uint32_t* packed2, const uint16_t* scales2, const uint8_t* zeros2, int group,
+                     uint16_t* dX, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * w4_gemm_dx_gated -- the down projection's input gradient carried through the gate, without
+ * storing it: dH = dY . W [M, K] (fp32), then
+ *     dG = dH * U * act'(G),  dU = dH * act(G).
+ *
+ *   dY [M, N] fp16; W [N, K] the down projection (K the gated block's inner size); G, U [M, K] fp16
+ *   as w4_gemm_gated wrote them; dG, dU [M, K] fp16 out.  dG may be G and dU may be U (in place).
+ * Errors: as w4_gemm; W4_ERR_UNSUPPORTED for an unknown activation.
+ */
+w4_status w4_gemm_dx_gated(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
+                           const uint16_t* scales, const uint8_t* zeros, int group, const uint16_t* G,
+                           const uint16_t* U, int activation, uint16_t* dG, uint16_t* dU, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace w4_act_backward needs when dbias is wanted (0 is enough otherwise). */
+w4_status w4_act_backward_workspace_size(int64_t M, int64_t N, size_t* bytes);
+
+/*
+ * w4_act_backward -- the activation's backward pass alone.
+ *
+ * U NULL (w4_gemm_fused):  dZ = dY * act'(Z); dbias[n] = sum_m dZ[m, n] (fp32, before dZ's rounding).
+ * U given (w4_gemm_gated): Z holds G and dY the gradient of H: dZ = dY * U * act'(Z) (that is dG),
+ *                          dU = dY * act(Z).
+ *   dY, Z, U [M, N] fp16; dZ, dU [M, N] fp16 out; dbias [N] fp32 out or NULL.  Outputs may be the
+ *   inputs' own buffers (dZ on dY or Z, dU on U, ...), each wholly.  With W4_ACT_NONE and no U, Z
+ *   is not read and may be NULL, and dZ (equal to dY) may be NULL.  dU goes with U.
+ *   ws: w4_act_backward_workspace_size bytes when dbias is given, else unused.
+ * M == 0 with dbias writes zeros.  Errors: W4_ERR_UNSUPPORTED for an unknown activation or for
+ * dbias together with U; else as w4_gemm.
+ */
+w4_status w4_act_backward(const uint16_t* dY, const uint16_t* Z, const uint16_t* U, int64_t M, int64_t N,
+                          int activation, uint16_t* dZ, uint16_t* dU, float* dbias, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
  * w4_selftest_bounded_wait -- self-test of the library's bounded waits (no counterpart on the
  * pages).  Launches one kernel that waits on a barrier nothing ever arrives at; after limit_ns
  * (1 us .. 5 s, else W4_ERR_UNSUPPORTED) the wait gives up, W4_ERR_DEVICE_TIMEOUT is recorded in

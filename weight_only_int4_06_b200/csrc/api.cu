@@ -550,6 +550,181 @@ w4_status awq_clip_search(const uint16_t* X, int64_t T, const uint16_t* W, int64
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ feed-forward operators
+static bool act_ok(int a) { return a >= W4_ACT_NONE && a <= W4_ACT_SILU; }
+
+static w4_status ffn_shape(int64_t M, int64_t N, int64_t K, int group) {
+    if (group != 128) return W4_ERR_UNSUPPORTED;
+    if (!dims_ok(M, K) || !dims_ok(N, K) || !dims_ok(M, N) || K % group != 0 || N % 8 != 0) return W4_ERR_SHAPE;
+    return W4_OK;
+}
+
+static w4_status ws_check(size_t need, const void* ws, size_t ws_bytes) {
+    if (ws_bytes < need) return W4_ERR_WORKSPACE;
+    if (need > 0 && !ws) return W4_ERR_NULL;
+    if (need > 0 && !aligned16(ws)) return W4_ERR_ALIGN;
+    return W4_OK;
+}
+
+static bool layer_null(const W4Layer& w) { return !w.packed || !w.scales || !w.zeros; }
+
+static cudaError_t zero_half(uint16_t* p, int64_t rows, int64_t cols, cudaStream_t s) {
+    return rows == 0 || cols == 0 ? cudaSuccess : cudaMemsetAsync(p, 0, (size_t)rows * (size_t)cols * 2, s);
+}
+
+w4_status w4_gemm_fused_workspace_size(int64_t M, int64_t N, int64_t K, int group, size_t* bytes) {
+    if (!bytes) return W4_ERR_NULL;
+    const w4_status st = ffn_shape(M, N, K, group);
+    if (st != W4_OK) return st;
+    *bytes = 0;
+    return W4_OK;
+}
+
+w4_status w4_gemm_fused(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
+                        const uint16_t* scales, const uint8_t* zeros, int group, const uint16_t* bias,
+                        int activation, const uint16_t* residual, uint16_t* Y, uint16_t* Z, void* ws,
+                        size_t ws_bytes, int flags, void* stream) {
+    if (!act_ok(activation) || (flags & ~W4_FLAG_WEIGHTS_STATIC) != 0) return W4_ERR_UNSUPPORTED;
+    size_t need = 0;
+    w4_status st = w4_gemm_fused_workspace_size(M, N, K, group, &need);
+    if (st == W4_OK) st = ws_check(need, ws, ws_bytes);
+    if (st != W4_OK) return st;
+    if (M == 0 || N == 0) return W4_OK;
+    const W4Layer w = {packed, scales, zeros};
+    if (!Y || (K > 0 && (!X || layer_null(w)))) return W4_ERR_NULL;
+    if (!aligned16(Y) || !aligned16(bias) || !aligned16(residual) || !aligned16(Z) ||
+        (K > 0 && (!aligned16(X) || !aligned16(packed))))
+        return W4_ERR_ALIGN;
+    int* status = device_status_ptr();
+    if (!status) return W4_ERR_CUDA;
+    const W4Epilogue ep = {bias, residual, activation, Y, Z, nullptr};
+    const cudaError_t e = launch_fused_simple(X, M, N, K, w, nullptr, ep, (cudaStream_t)stream);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+w4_status w4_gemm_gated_workspace_size(int64_t M, int64_t N, int64_t K, int group, size_t* bytes) {
+    if (!bytes) return W4_ERR_NULL;
+    const w4_status st = ffn_shape(M, N, K, group);
+    if (st != W4_OK) return st;
+    *bytes = 0;
+    return W4_OK;
+}
+
+w4_status w4_gemm_gated(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* gate_packed,
+                        const uint16_t* gate_scales, const uint8_t* gate_zeros, const uint32_t* up_packed,
+                        const uint16_t* up_scales, const uint8_t* up_zeros, int group, int activation,
+                        uint16_t* H, uint16_t* G, uint16_t* U, void* ws, size_t ws_bytes, int flags,
+                        void* stream) {
+    if (!act_ok(activation) || (flags & ~W4_FLAG_WEIGHTS_STATIC) != 0) return W4_ERR_UNSUPPORTED;
+    size_t need = 0;
+    w4_status st = w4_gemm_gated_workspace_size(M, N, K, group, &need);
+    if (st == W4_OK) st = ws_check(need, ws, ws_bytes);
+    if (st != W4_OK) return st;
+    if (M == 0 || N == 0) return W4_OK;
+    const W4Layer wg = {gate_packed, gate_scales, gate_zeros}, wu = {up_packed, up_scales, up_zeros};
+    if (!H || !G != !U || (K > 0 && (!X || layer_null(wg) || layer_null(wu)))) return W4_ERR_NULL;
+    if (!aligned16(H) || !aligned16(G) || !aligned16(U) ||
+        (K > 0 && (!aligned16(X) || !aligned16(gate_packed) || !aligned16(up_packed))))
+        return W4_ERR_ALIGN;
+    int* status = device_status_ptr();
+    if (!status) return W4_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (K == 0) {  // empty sums: act(0) * 0
+        for (uint16_t* out : {H, G, U})
+            if (out && zero_half(out, M, N, s) != cudaSuccess) return W4_ERR_CUDA;
+        return W4_OK;
+    }
+    const W4Epilogue ep = {nullptr, nullptr, activation, H, G, U};
+    const cudaError_t e = launch_fused_simple(X, M, N, K, wg, &wu, ep, s);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+w4_status w4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int n_layers, int group, size_t* bytes) {
+    if (!bytes) return W4_ERR_NULL;
+    if (n_layers != 1 && n_layers != 2) return W4_ERR_UNSUPPORTED;
+    const w4_status st = ffn_shape(M, N, K, group);
+    if (st != W4_OK) return st;
+    *bytes = 0;
+    return W4_OK;
+}
+
+w4_status w4_gemm_dx(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
+                     const uint16_t* scales, const uint8_t* zeros, const uint16_t* dY2,
+                     const uint32_t* packed2, const uint16_t* scales2, const uint8_t* zeros2, int group,
+                     uint16_t* dX, void* ws, size_t ws_bytes, void* stream) {
+    const bool two = dY2 || packed2 || scales2 || zeros2;
+    size_t need = 0;
+    w4_status st = w4_gemm_dx_workspace_size(M, N, K, two ? 2 : 1, group, &need);
+    if (st == W4_OK) st = ws_check(need, ws, ws_bytes);
+    if (st != W4_OK) return st;
+    const W4Layer w = {packed, scales, zeros}, w2 = {packed2, scales2, zeros2};
+    if (two && (!dY2 || layer_null(w2))) return W4_ERR_NULL;
+    if (M == 0 || K == 0) return W4_OK;
+    if (!dX || (N > 0 && (!dY || layer_null(w)))) return W4_ERR_NULL;
+    if (!aligned16(dX) || (N > 0 && (!aligned16(dY) || !aligned16(packed) || !aligned16(dY2) || !aligned16(packed2))))
+        return W4_ERR_ALIGN;
+    int* status = device_status_ptr();
+    if (!status) return W4_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (N == 0) return zero_half(dX, M, K, s) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+    const cudaError_t e = launch_dx_simple(dY, w, dY2, two ? &w2 : nullptr, M, N, K, nullptr, dX, s);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+w4_status w4_gemm_dx_gated(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
+                           const uint16_t* scales, const uint8_t* zeros, int group, const uint16_t* G,
+                           const uint16_t* U, int activation, uint16_t* dG, uint16_t* dU, void* ws,
+                           size_t ws_bytes, void* stream) {
+    if (!act_ok(activation)) return W4_ERR_UNSUPPORTED;
+    size_t need = 0;
+    w4_status st = w4_gemm_dx_workspace_size(M, N, K, 1, group, &need);
+    if (st == W4_OK) st = ws_check(need, ws, ws_bytes);
+    if (st != W4_OK) return st;
+    if (M == 0 || K == 0) return W4_OK;
+    const W4Layer w = {packed, scales, zeros};
+    if (!G || !U || !dG || !dU || (N > 0 && (!dY || layer_null(w)))) return W4_ERR_NULL;
+    if (!aligned16(G) || !aligned16(U) || !aligned16(dG) || !aligned16(dU) ||
+        (N > 0 && (!aligned16(dY) || !aligned16(packed))))
+        return W4_ERR_ALIGN;
+    int* status = device_status_ptr();
+    if (!status) return W4_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (N == 0)
+        return zero_half(dG, M, K, s) == cudaSuccess && zero_half(dU, M, K, s) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+    const W4GateGrad gate = {G, U, activation, dG, dU};
+    const cudaError_t e = launch_dx_simple(dY, w, nullptr, nullptr, M, N, K, &gate, nullptr, s);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+w4_status w4_act_backward_workspace_size(int64_t M, int64_t N, size_t* bytes) {
+    if (!bytes) return W4_ERR_NULL;
+    if (!dims_ok(M, N) || N % 8 != 0) return W4_ERR_SHAPE;
+    *bytes = act_backward_workspace(M, N);
+    return W4_OK;
+}
+
+w4_status w4_act_backward(const uint16_t* dY, const uint16_t* Z, const uint16_t* U, int64_t M, int64_t N,
+                          int activation, uint16_t* dZ, uint16_t* dU, float* dbias, void* ws,
+                          size_t ws_bytes, void* stream) {
+    if (!act_ok(activation) || (U && dbias)) return W4_ERR_UNSUPPORTED;
+    size_t need = 0;
+    w4_status st = w4_act_backward_workspace_size(M, N, &need);
+    if (st == W4_OK && dbias) st = ws_check(need, ws, ws_bytes);
+    if (st != W4_OK) return st;
+    if (N == 0 || (M == 0 && !dbias)) return W4_OK;
+    if (!aligned16(dbias)) return W4_ERR_ALIGN;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (M == 0)  // an empty sum
+        return cudaMemsetAsync(dbias, 0, (size_t)N * 4, s) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+    const bool identity = activation == W4_ACT_NONE && !U;  // dZ == dY
+    if (!dY || (!identity && (!Z || !dZ)) || !U != !dU) return W4_ERR_NULL;
+    if (!aligned16(dY) || !aligned16(Z) || !aligned16(U) || !aligned16(dZ) || !aligned16(dU)) return W4_ERR_ALIGN;
+    if (identity && !dZ && !dbias) return W4_OK;
+    const cudaError_t e =
+        launch_act_backward(dY, identity ? nullptr : Z, U, M, N, activation, dZ, dU, dbias, ws, s);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
 w4_status w4_check_device_status(void* stream) {
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return W4_ERR_CUDA;
     int* p = device_status_ptr();

@@ -7,6 +7,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "w4a16.h"
 
 namespace w4 {
@@ -188,5 +190,53 @@ AwqClipLayout awq_clip_layout(int64_t T, int64_t N, int64_t K, int n_ratios);
 cudaError_t launch_awq_clip(const uint16_t* X, int64_t T, const uint16_t* W, int64_t N, int64_t K, int n_ratios,
                             const float* act_scale, uint8_t* best_idx, float* err, uint32_t* packed,
                             uint16_t* scales, uint8_t* zeros, void* ws, int* status, cudaStream_t stream);
+
+// ------------------------------------------------------------------ feed-forward operators
+// One quantised layer's weights.
+struct W4Layer {
+    const uint32_t* packed;
+    const uint16_t* scales;
+    const uint8_t* zeros;
+};
+// What follows the product of w4_gemm_fused / w4_gemm_gated (null pointers: absent).
+struct W4Epilogue {
+    const uint16_t* bias;
+    const uint16_t* residual;
+    int activation;
+    uint16_t* Y;  // gated: H
+    uint16_t* Z;  // pre-activation; gated: G
+    uint16_t* U;  // gated only
+};
+// The gate's backward pass behind an input-gradient product (w4_gemm_dx_gated).
+struct W4GateGrad {
+    const uint16_t* G;
+    const uint16_t* U;
+    int activation;
+    uint16_t* dG;
+    uint16_t* dU;
+};
+// Calls f with the activation as a compile-time constant.
+template <typename F>
+cudaError_t dispatch_act(int activation, F&& f) {
+    switch (activation) {
+        case W4_ACT_NONE: return f(std::integral_constant<int, W4_ACT_NONE>{});
+        case W4_ACT_RELU: return f(std::integral_constant<int, W4_ACT_RELU>{});
+        case W4_ACT_GELU: return f(std::integral_constant<int, W4_ACT_GELU>{});
+        case W4_ACT_GELU_TANH: return f(std::integral_constant<int, W4_ACT_GELU_TANH>{});
+        case W4_ACT_SILU: return f(std::integral_constant<int, W4_ACT_SILU>{});
+    }
+    return cudaErrorInvalidValue;
+}
+// ffn_simple.cu: w2 null: fused; else gated (w the gate, w2 the up projection).
+cudaError_t launch_fused_simple(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
+                                const W4Epilogue& ep, cudaStream_t stream);
+// dX = dY W (+ dY2 w2), or with `gate` dG and dU from dH = dY W.
+cudaError_t launch_dx_simple(const uint16_t* dY, const W4Layer& w, const uint16_t* dY2, const W4Layer* w2, int64_t M,
+                             int64_t N, int64_t K, const W4GateGrad* gate, uint16_t* dX, cudaStream_t stream);
+// act_backward.cu
+size_t act_backward_workspace(int64_t M, int64_t N);  // bytes, for dbias
+cudaError_t launch_act_backward(const uint16_t* dY, const uint16_t* Z, const uint16_t* U, int64_t M, int64_t N,
+                                int activation, uint16_t* dZ, uint16_t* dU, float* dbias, void* ws,
+                                cudaStream_t stream);
 
 }  // namespace w4

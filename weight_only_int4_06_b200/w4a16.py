@@ -6,6 +6,7 @@ no fallback: if libw4a16.so is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -21,6 +22,8 @@ STATUS_NAMES = {
 }
 VARIANT_AUTO, VARIANT_SKINNY, VARIANT_TC, VARIANT_GEMV, VARIANT_GEMV_TC = 0, 1, 2, 3, 4
 FLAG_WEIGHTS_STATIC = 0x100
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
 
 # Entry points declared in include/w4a16.h: (name, restype, argtypes)
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -51,6 +54,16 @@ SIGNATURES = {
     "awq_sse_workspace_size": (_I32, [_I64, _I64, _I64, _I32, _I32, ctypes.POINTER(_SZ)]),
     "awq_sse": (_I32, [_P, _I64, _P, _I64, _I64, _I32, _I32, _P, _P, _P, _SZ, _P]),
     "awq_select": (_I32, [_P, _I32, _I32, _I64, _I64, _P, _I64, _P, _P, _P, _P]),
+    "w4_gemm_fused_workspace_size": (_I32, [_I64, _I64, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "w4_gemm_fused": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, _SZ, _I32, _P]),
+    "w4_gemm_gated_workspace_size": (_I32, [_I64, _I64, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "w4_gemm_gated": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _I32, _P, _P, _P, _P, _SZ, _I32,
+                             _P]),
+    "w4_gemm_dx_workspace_size": (_I32, [_I64, _I64, _I64, _I32, _I32, ctypes.POINTER(_SZ)]),
+    "w4_gemm_dx": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _SZ, _P]),
+    "w4_gemm_dx_gated": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _SZ, _P]),
+    "w4_act_backward_workspace_size": (_I32, [_I64, _I64, ctypes.POINTER(_SZ)]),
+    "w4_act_backward": (_I32, [_P, _P, _P, _I64, _I64, _I32, _P, _P, _P, _P, _SZ, _P]),
     "w4_selftest_bounded_wait": (_I32, [ctypes.c_uint64, _P]),
     "awq_clip_workspace_size": (_I32, [_I64, _I64, _I64, _I32, _I32, ctypes.POINTER(_SZ)]),
     "awq_clip_search": (_I32, [_P, _I64, _P, _I64, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -601,6 +614,237 @@ def awq_clip_search(X: torch.Tensor, W: torch.Tensor, act_scale: torch.Tensor | 
                                workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "awq_clip_search")
     return best, err, packed, scales, zeros
+
+
+# ------------------------------------------------------------------ feed-forward operators
+def _arg(t: torch.Tensor, dtype, shape, dev, name) -> int:
+    """Device address of a tensor argument, its type, shape, device and layout checked."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _layer_args(layer, N: int, K: int, group: int, dev, name: str):
+    packed, scales, zeros = layer
+    G = K // group if group > 0 else 0
+    return (_arg(packed, torch.int32, (N, K // 8), dev, name + "packed"),
+            _arg(scales, torch.float16, (N, G), dev, name + "scales"),
+            _arg(zeros, torch.uint8, (N, G), dev, name + "zeros"))
+
+
+def _raw_stream(dev, stream) -> int:
+    """The cudaStream_t of `stream`, or of the device's current stream."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _on(dev, stream):
+    """Context in which a call allocates and launches: the tensors' device, and `stream` when one is
+    given (so that new outputs and workspaces belong to it)."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != dev.index:
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+_ffn_ws_cache: dict = {}
+
+
+def _ffn_workspace(name: str, dims: tuple, workspace, dev):
+    """(address, bytes) of the caller's workspace or, where it has none or one too small, of a new
+    one, and the tensor that holds it."""
+    need = _ffn_ws_cache.get((name, dims))
+    if need is None:
+        n = ctypes.c_size_t(0)
+        _check(getattr(lib(), name)(*dims, ctypes.byref(n)), name)
+        need = _ffn_ws_cache[(name, dims)] = n.value
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        have = workspace.numel() * workspace.element_size()
+        if have >= need:
+            return workspace.data_ptr(), have, workspace
+    if need == 0:
+        return None, 0, None
+    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace.data_ptr(), need, workspace
+
+
+def _out(t, shape, dev, name):
+    """An output tensor (a new one when none is given) and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=torch.float16, device=dev)
+        return t, t.data_ptr()
+    return t, _arg(t, torch.float16, shape, dev, name)
+
+
+def _on_gpu(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def w4_gemm_fused_workspace_size(M: int, N: int, K: int, group: int = 128) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().w4_gemm_fused_workspace_size(M, N, K, group, ctypes.byref(n)), "w4_gemm_fused_workspace_size")
+    return n.value
+
+
+def w4_gemm_fused(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                  bias: torch.Tensor | None = None, activation: int = ACT_NONE,
+                  residual: torch.Tensor | None = None, save_pre: bool = False, group: int = 128,
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, flags: int = 0,
+                  stream=None):
+    """Y = act(X . dequant(W)^T + bias) + residual; with save_pre (Y, Z), Z = X . dequant(W)^T + bias.
+    `out` may be the residual (added in place)."""
+    M, K = _matrix(X, "X")
+    N = _matrix(packed, "packed")[0]
+    dev = _on_gpu(X, "X")
+    xp = _arg(X, torch.float16, (M, K), dev, "X")
+    wp, sp, zp = _layer_args((packed, scales, zeros), N, K, group, dev, "")
+    bp = _arg(bias, torch.float16, (N,), dev, "bias") if bias is not None else None
+    rp = _arg(residual, torch.float16, (M, N), dev, "residual") if residual is not None else None
+    with _on(dev, stream):
+        wsp, wsb, workspace = _ffn_workspace("w4_gemm_fused_workspace_size", (M, N, K, group), workspace, dev)
+        Y, yp = _out(out, (M, N), dev, "out")
+        Z, pre = _out(None, (M, N), dev, "Z") if save_pre else (None, None)
+        _check(lib().w4_gemm_fused(xp, M, N, K, wp, sp, zp, group, bp, activation, rp, yp, pre, wsp, wsb, flags,
+                                   _raw_stream(dev, stream)), "w4_gemm_fused")
+    return (Y, Z) if save_pre else Y
+
+
+def w4_gemm_gated_workspace_size(M: int, N: int, K: int, group: int = 128) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().w4_gemm_gated_workspace_size(M, N, K, group, ctypes.byref(n)), "w4_gemm_gated_workspace_size")
+    return n.value
+
+
+def w4_gemm_gated(X: torch.Tensor, gate, up, activation: int = ACT_SILU, save_pre: bool = False, group: int = 128,
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, flags: int = 0,
+                  stream=None):
+    """H = act(X . Wg^T) * (X . Wu^T); gate and up: (packed, scales, zeros) each.  With save_pre
+    (H, G, U), the two projections that the backward pass takes."""
+    M, K = _matrix(X, "X")
+    N = _matrix(gate[0], "gate packed")[0]
+    dev = _on_gpu(X, "X")
+    xp = _arg(X, torch.float16, (M, K), dev, "X")
+    g = _layer_args(gate, N, K, group, dev, "gate ")
+    u = _layer_args(up, N, K, group, dev, "up ")
+    with _on(dev, stream):
+        wsp, wsb, workspace = _ffn_workspace("w4_gemm_gated_workspace_size", (M, N, K, group), workspace, dev)
+        H, hp = _out(out, (M, N), dev, "out")
+        G, gp = _out(None, (M, N), dev, "G") if save_pre else (None, None)
+        U, up_ = _out(None, (M, N), dev, "U") if save_pre else (None, None)
+        _check(lib().w4_gemm_gated(xp, M, N, K, *g, *u, group, activation, hp, gp, up_, wsp, wsb, flags,
+                                   _raw_stream(dev, stream)), "w4_gemm_gated")
+    return (H, G, U) if save_pre else H
+
+
+def w4_gemm_dx_workspace_size(M: int, N: int, K: int, n_layers: int = 1, group: int = 128) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().w4_gemm_dx_workspace_size(M, N, K, n_layers, group, ctypes.byref(n)), "w4_gemm_dx_workspace_size")
+    return n.value
+
+
+def w4_gemm_dx(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+               dY2: torch.Tensor | None = None, weights2=None, group: int = 128, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dX = dY . dequant(W) (+ dY2 . dequant(W2), weights2 = (packed, scales, zeros)), [M, K]."""
+    M, N = _matrix(dY, "dY")
+    K = _matrix(packed, "packed")[1] * 8
+    dev = _on_gpu(dY, "dY")
+    yp = _arg(dY, torch.float16, (M, N), dev, "dY")
+    w = _layer_args((packed, scales, zeros), N, K, group, dev, "")
+    if (dY2 is None) != (weights2 is None):
+        raise ValueError("dY2 and weights2 go together")
+    yp2, w2 = None, (None, None, None)
+    if dY2 is not None:
+        yp2 = _arg(dY2, torch.float16, (M, N), dev, "dY2")
+        w2 = _layer_args(weights2, N, K, group, dev, "second ")
+    with _on(dev, stream):
+        wsp, wsb, workspace = _ffn_workspace("w4_gemm_dx_workspace_size", (M, N, K, 1 if dY2 is None else 2, group),
+                                             workspace, dev)
+        dX, xp = _out(out, (M, K), dev, "out")
+        _check(lib().w4_gemm_dx(yp, M, N, K, *w, yp2, *w2, group, xp, wsp, wsb, _raw_stream(dev, stream)),
+               "w4_gemm_dx")
+    return dX
+
+
+def w4_gemm_dx_gated(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                     G: torch.Tensor, U: torch.Tensor, activation: int = ACT_SILU, group: int = 128, out=None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """(dG, dU) [M, K] from dH = dY . dequant(W): dG = dH U act'(G), dU = dH act(G).  out = (dG, dU)
+    may be (G, U) (in place)."""
+    M, N = _matrix(dY, "dY")
+    K = _matrix(packed, "packed")[1] * 8
+    dev = _on_gpu(dY, "dY")
+    yp = _arg(dY, torch.float16, (M, N), dev, "dY")
+    w = _layer_args((packed, scales, zeros), N, K, group, dev, "")
+    gp = _arg(G, torch.float16, (M, K), dev, "G")
+    up = _arg(U, torch.float16, (M, K), dev, "U")
+    with _on(dev, stream):
+        wsp, wsb, workspace = _ffn_workspace("w4_gemm_dx_workspace_size", (M, N, K, 1, group), workspace, dev)
+        dG, dgp = _out(out[0] if out is not None else None, (M, K), dev, "out[0]")
+        dU, dup = _out(out[1] if out is not None else None, (M, K), dev, "out[1]")
+        _check(lib().w4_gemm_dx_gated(yp, M, N, K, *w, group, gp, up, activation, dgp, dup, wsp, wsb,
+                                      _raw_stream(dev, stream)), "w4_gemm_dx_gated")
+    return dG, dU
+
+
+def w4_act_backward_workspace_size(M: int, N: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().w4_act_backward_workspace_size(M, N, ctypes.byref(n)), "w4_act_backward_workspace_size")
+    return n.value
+
+
+def w4_act_backward(dY: torch.Tensor, Z: torch.Tensor | None, U: torch.Tensor | None = None,
+                    activation: int = ACT_SILU, bias_grad: bool = False, out=None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """The activation's backward pass.  Without U: dZ = dY act'(Z), and with bias_grad (dZ, dbias), dbias [N]
+    fp32 the column sums of dZ.  With U (gated: Z is G): (dG, dU) = (dY U act'(Z), dY act(Z)).
+    out: dZ, or (dG, dU), possibly the inputs' own buffers.  With ACT_NONE and no U, Z may be None."""
+    M, N = _matrix(dY, "dY")
+    dev = _on_gpu(dY, "dY")
+    yp = _arg(dY, torch.float16, (M, N), dev, "dY")
+    zp = _arg(Z, torch.float16, (M, N), dev, "Z") if Z is not None else None
+    up = _arg(U, torch.float16, (M, N), dev, "U") if U is not None else None
+    if U is None:
+        out = (out, None)
+    elif out is None:
+        out = (None, None)
+    with _on(dev, stream):
+        dZ, dzp = _out(out[0], (M, N), dev, "out")
+        dU, dup = _out(out[1], (M, N), dev, "out[1]") if U is not None else (None, None)
+        dbias = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
+        wsp, wsb = None, 0
+        if bias_grad:
+            wsp, wsb, workspace = _ffn_workspace("w4_act_backward_workspace_size", (M, N), workspace, dev)
+        _check(lib().w4_act_backward(yp, zp, up, M, N, activation, dzp, dup,
+                                     dbias.data_ptr() if bias_grad else None, wsp, wsb, _raw_stream(dev, stream)),
+               "w4_act_backward")
+    if U is not None:
+        return dZ, dU
+    return (dZ, dbias) if bias_grad else dZ
 
 
 def w4_check_device_status(stream=None) -> int:
