@@ -576,7 +576,7 @@ w4_status w4_gemm_fused_workspace_size(int64_t M, int64_t N, int64_t K, int grou
     if (!bytes) return W4_ERR_NULL;
     const w4_status st = ffn_shape(M, N, K, group);
     if (st != W4_OK) return st;
-    *bytes = 0;
+    *bytes = M > 0 && N > 0 && K > 0 ? ffn_gemm_workspace(M, N, K, false) : 0;
     return W4_OK;
 }
 
@@ -598,7 +598,10 @@ w4_status w4_gemm_fused(const uint16_t* X, int64_t M, int64_t N, int64_t K, cons
     int* status = device_status_ptr();
     if (!status) return W4_ERR_CUDA;
     const W4Epilogue ep = {bias, residual, activation, Y, Z, nullptr};
-    const cudaError_t e = launch_fused_simple(X, M, N, K, w, nullptr, ep, (cudaStream_t)stream);
+    cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = K == 0 ? launch_ffn_reduce(nullptr, 0, M, N, false, ep, s)  // the epilogue of an empty sum
+                                 : launch_ffn_gemm(X, M, N, K, w, nullptr, ep, ws, (flags & W4_FLAG_WEIGHTS_STATIC) != 0,
+                                                   status, s);
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
@@ -606,7 +609,7 @@ w4_status w4_gemm_gated_workspace_size(int64_t M, int64_t N, int64_t K, int grou
     if (!bytes) return W4_ERR_NULL;
     const w4_status st = ffn_shape(M, N, K, group);
     if (st != W4_OK) return st;
-    *bytes = 0;
+    *bytes = M > 0 && N > 0 && K > 0 ? ffn_gemm_workspace(M, N, K, true) : 0;
     return W4_OK;
 }
 
@@ -635,7 +638,8 @@ w4_status w4_gemm_gated(const uint16_t* X, int64_t M, int64_t N, int64_t K, cons
         return W4_OK;
     }
     const W4Epilogue ep = {nullptr, nullptr, activation, H, G, U};
-    const cudaError_t e = launch_fused_simple(X, M, N, K, wg, &wu, ep, s);
+    const cudaError_t e =
+        launch_ffn_gemm(X, M, N, K, wg, &wu, ep, ws, (flags & W4_FLAG_WEIGHTS_STATIC) != 0, status, s);
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 

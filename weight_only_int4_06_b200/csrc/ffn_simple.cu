@@ -1,9 +1,7 @@
-// The feed-forward operators as plain tiled products on the CUDA cores: 64 x 64 output tiles, 4 x 4
-// fp32 sums per thread, the contraction in steps of 16 through shared memory.  Every weight is
-// (q - z) * s in fp32 (exact), every sum fp32, one rounding at the store.
-//
-// Modes: forward (Y[m, n] = sum_k X[m, k] W[n, k], one or two layers) and input gradient
-// (dX[m, k] = sum_n dY[m, n] W[n, k], one layer or the sum of two).
+// Input gradients dX[m, k] = sum_n dY[m, n] W[n, k] (one layer or the sum of two) as plain tiled
+// products on the CUDA cores: 64 x 64 output tiles, 4 x 4 fp32 sums per thread, the contraction in
+// steps of 16 through shared memory.  Every weight is (q - z) * s in fp32 (exact), every sum fp32,
+// one rounding at the store.
 #include "activation.cuh"
 #include "internal.h"
 
@@ -52,30 +50,6 @@ __device__ __forceinline__ void simple_tile(const __half* A, const Layer& w, int
     }
 }
 
-template <int ACT, bool GATED>
-__global__ void __launch_bounds__(256) simple_forward_kernel(const __half* X, Layer w, Layer w2, int64_t M, int64_t N,
-                                                             int64_t K, const __half* bias, const __half* residual,
-                                                             __half* Y, __half* Z, __half* U) {
-    __shared__ float sa[SK][ST + 1], sb[SK][ST + 1];
-    const int64_t m0 = (int64_t)blockIdx.y * ST, n0 = (int64_t)blockIdx.x * ST;
-    float acc[4][4] = {}, acc2[4][4] = {};
-    simple_tile<false>(X, w, M, N, K, m0, n0, acc, sa, sb);
-    if (GATED) simple_tile<false>(X, w2, M, N, K, m0, n0, acc2, sa, sb);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + (threadIdx.x >> 4) * 4 + i, n = n0 + (threadIdx.x & 15) * 4 + j;
-            if (m >= M || n >= N) continue;
-            float z = acc[i][j];
-            if (bias) z += __half2float(bias[n]);
-            float y = act_fwd<ACT>(z);
-            if (GATED) y *= acc2[i][j];
-            if (residual) y += __half2float(residual[m * N + n]);
-            Y[m * N + n] = __float2half_rn(y);
-            if (Z) Z[m * N + n] = __float2half_rn(z);
-            if (U) U[m * N + n] = __float2half_rn(acc2[i][j]);
-        }
-}
-
 // ACT < 0: dX itself; else the gate's backward pass on it.
 template <int ACT>
 __global__ void __launch_bounds__(256) simple_dx_kernel(const __half* dY, Layer w, const __half* dY2, Layer w2, int64_t M,
@@ -108,22 +82,6 @@ const __half* h(const uint16_t* p) { return reinterpret_cast<const __half*>(p); 
 __half* h(uint16_t* p) { return reinterpret_cast<__half*>(p); }
 
 }  // namespace
-
-cudaError_t launch_fused_simple(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
-                                const W4Epilogue& ep, cudaStream_t stream) {
-    const dim3 grid((unsigned)((N + ST - 1) / ST), (unsigned)((M + ST - 1) / ST));
-    const Layer a = layer(w), b = w2 ? layer(*w2) : a;
-    return dispatch_act(ep.activation, [&](auto act) {
-        constexpr int ACT = decltype(act)::value;
-        if (w2)
-            simple_forward_kernel<ACT, true><<<grid, 256, 0, stream>>>(h(X), a, b, M, N, K, h(ep.bias), h(ep.residual),
-                                                                        h(ep.Y), h(ep.Z), h(ep.U));
-        else
-            simple_forward_kernel<ACT, false><<<grid, 256, 0, stream>>>(h(X), a, b, M, N, K, h(ep.bias), h(ep.residual),
-                                                                         h(ep.Y), h(ep.Z), h(ep.U));
-        return cudaGetLastError();
-    });
-}
 
 cudaError_t launch_dx_simple(const uint16_t* dY, const W4Layer& w, const uint16_t* dY2, const W4Layer* w2, int64_t M,
                              int64_t N, int64_t K, const W4GateGrad* gate, uint16_t* dX, cudaStream_t stream) {

@@ -217,7 +217,7 @@ struct W4GateGrad {
 };
 // Calls f with the activation as a compile-time constant.
 template <typename F>
-cudaError_t dispatch_act(int activation, F&& f) {
+__host__ __device__ inline cudaError_t dispatch_act(int activation, F&& f) {
     switch (activation) {
         case W4_ACT_NONE: return f(std::integral_constant<int, W4_ACT_NONE>{});
         case W4_ACT_RELU: return f(std::integral_constant<int, W4_ACT_RELU>{});
@@ -227,9 +227,15 @@ cudaError_t dispatch_act(int activation, F&& f) {
     }
     return cudaErrorInvalidValue;
 }
-// ffn_simple.cu: w2 null: fused; else gated (w the gate, w2 the up projection).
-cudaError_t launch_fused_simple(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
-                                const W4Epilogue& ep, cudaStream_t stream);
+// ffn_gemm.cu: w2 null: fused; else gated (w the gate, w2 the up projection).  ws: ffn_gemm_workspace
+// bytes (fp32 sums of the K slices), may be null when that is 0.
+size_t ffn_gemm_workspace(int64_t M, int64_t N, int64_t K, bool gated);
+cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
+                            const W4Epilogue& ep, void* ws, bool weights_static, int* status, cudaStream_t stream);
+// The epilogue of the sum of `slices` partial products P [slice][layer][M][N], in slice order.
+cudaError_t launch_ffn_reduce(const float* P, int slices, int64_t M, int64_t N, bool gated, const W4Epilogue& ep,
+                              cudaStream_t stream);
+// ffn_simple.cu
 // dX = dY W (+ dY2 w2), or with `gate` dG and dU from dH = dY W.
 cudaError_t launch_dx_simple(const uint16_t* dY, const W4Layer& w, const uint16_t* dY2, const W4Layer* w2, int64_t M,
                              int64_t N, int64_t K, const W4GateGrad* gate, uint16_t* dX, cudaStream_t stream);
