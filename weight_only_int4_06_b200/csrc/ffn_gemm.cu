@@ -17,17 +17,22 @@
 // small batches cost products of 32 columns, not 128.
 //
 //   warp 0       TMA producer of its CTA: per group X (two boxes of 64 k) and the packed rows
-//   warp 1       CTA 0: one thread issues the pair's tcgen05.mma (M = 256, N = tn, K = 16)
+//   warp 1       CTA 0: issues the pair's tcgen05.mma (M = 256, N = tn, K = 16) and one commit a group
 //   warp 2       TMEM allocation
-//   warps 4-11   dequantise: the first four warps each group's k 0-63, the other four its k 64-127;
-//                64 codes of a row -> 32 TMEM columns
-//   warps 12-19  fold: the first four take columns 0 .. tn/2 - 1, the others the rest: read a group's
-//                sums from TMEM, acc += s * sum in registers; after the last group the epilogue
-// The group sums alternate between two TMEM buffers, the dequantised halves between four, so a
-// group's products, the next one's dequantisation and the last one's fold overlap.
+//   next 4 DW    dequantise: 4 warps take a group's k 0-63, 4 its k 64-127 (a row's 64 codes -> 32 TMEM
+//                columns); with DW = 4 two such pairs alternate between groups
+//   last 8       fold: four take columns 0 .. tn/2 - 1, four the rest: read a group's sums from TMEM,
+//                acc += s * sum in registers; after the last group the epilogue
+// The group sums rotate through NB TMEM buffers, the dequantised groups through AG, so a group's
+// products, the next ones' dequantisation and the last one's fold overlap.  One barrier per ring
+// stage (committed once by the tensor cores) tells the producer that the stage, the dequantising warps
+// that the group's TMEM columns are free, and the fold warps that the sums are there.
 //
-// Gated: the 32 lanes of a warp hold 16 gate rows and the 16 up rows of the same n, so g and u of an
-// output meet by one shuffle between lanes i and i + 16.
+// Epilogue: the fold warps pass 32 columns at a time through shared memory as fp32 [m][n], so that the
+// output, residual and pre-activation rows are read and written as whole 256-byte rows (from the
+// accumulators' own layout, thread = n, a warp's stores were 64-byte pieces: 25 cycles each).
+// Gated: the 32 lanes of a warp hold 16 gate rows and the 16 up rows of the same n, so both factors of
+// an output lie in one CTA's rows.
 //
 // Few tiles: K is cut into slices of whole groups, their fp32 sums go to the workspace [slice][layer]
 // [M][N] and ffn_reduce_kernel adds them in slice order and runs the epilogue: deterministic.
@@ -44,14 +49,27 @@ namespace w4 {
 
 namespace {
 
-constexpr int FG_THREADS = 640;
 constexpr int FG_MAXS = 16;                        // ring stages at most
 constexpr uint32_t FG_P_BYTES = 128 * 64;          // packed codes of one group: 128 rows x 64 bytes
 constexpr uint32_t FG_SMEM = 227 * 1024;
-constexpr int FG_ASLOTS = 4;                       // dequantised half groups (32 TMEM columns each)
-// registers per thread: launch allotment 96 x 640; the fold warps' accumulators take what the others
-// give up (32 + 72 + 72 + 152 + 152 = 5 x 96)
-constexpr int FG_REGS_LAUNCH = 96, FG_REGS_MISC = 32, FG_REGS_DEQ = 72, FG_REGS_FOLD = 152;
+constexpr uint32_t FG_EPI = 32 * 128 * 4;          // a fold warpgroup's 32 rows of 128 fp32
+
+// NMAX columns at most.  192 (large batches): 96 accumulators per fold thread.  64 (small ones): twice
+// the dequantising warps, which bound it, and twice the TMEM buffers.  Every thread launches with
+// kRegs registers; the fold warps take what the others give up (in warpgroup shares: 24 + 2 x 64 + 2 x
+// 160 = 472 of 5 x 96, and 24 + 4 x 64 + 2 x 112 = 504 of 7 x 72).
+template <int NMAX>
+struct FgCfg {
+    static constexpr bool kWide = NMAX > 64;
+    static constexpr int kDW = kWide ? 2 : 4;       // dequantising warpgroups
+    static constexpr int kNB = kWide ? 2 : 4;       // TMEM buffers of group sums
+    static constexpr int kAG = kWide ? 2 : 4;       // dequantised groups in TMEM (64 columns each)
+    static constexpr int kThreads = 128 * (1 + kDW + 2);
+    static constexpr uint32_t kACol = kNB * NMAX;   // 384 or 256; + 64 kAG = 512
+    static constexpr int kRegs = kWide ? 96 : 72;
+    static constexpr int kRegsMisc = 24, kRegsDeq = 64, kRegsFold = kWide ? 160 : 112;
+    static_assert(kRegsMisc + kDW * kRegsDeq + 2 * kRegsFold <= (3 + kDW) * kRegs, "register shares");
+};
 
 struct FgArgs {
     const unsigned short* s0;
@@ -128,113 +146,141 @@ __device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
 
-// One tile's outputs from this thread's accumulators: weight row / output column n, X rows m0 ..
-// m0 + 16 NCH - 1 (acc[c]).  Lanes of a warp are neighbouring n: stores of one m are contiguous.
-template <int ACT, int NACC>
-__device__ __forceinline__ void fg_epilogue_plain(const FgArgs& p, const uint64_t (&acc)[NACC / 2], int ncol, int m0, int n) {
-    if (n >= p.N) return;
-    const float b = p.bias ? __half2float(p.bias[n]) : 0.0f;
-    const int64_t o = (int64_t)m0 * p.N + n;
-    __half* y = p.Y + o;
-    __half* z = p.Z ? p.Z + o : nullptr;
-    const __half* r = p.residual ? p.residual + o : nullptr;
-    const int rows = min(ncol, p.M - m0);
-#pragma unroll
-    for (int c = 0; c < NACC; c += 8) {
-        if (c < rows) {
-            float res[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                res[i] = r && c + i < rows ? __half2float(*r) : 0.0f;
-                if (r) r += p.N;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float v[2];
-                unpack_f32x2(acc[(c + i) / 2], v[0], v[1]);
-                const float pre = v[i & 1] + b;
-                if (c + i < rows) {
-                    *y = __float2half_rn(act_fwd<ACT>(pre) + res[i]);
-                    if (z) *z = __float2half_rn(pre);
-                }
-                y += p.N;
-                if (z) z += p.N;
-            }
-        }
-    }
+// 16 columns' sums, ordered before their use by the wait.
+__device__ __forceinline__ void fg_tie(uint32_t (&v)[16]) {
+    asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                      "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
 }
 
-// Gated: lanes 0-15 hold g, lanes 16-31 u of the same 16 columns n; a lower lane finishes the even X
-// row of each pair, an upper lane the odd one.
-template <int ACT, int NACC>
-__device__ __forceinline__ void fg_epilogue_gated(const FgArgs& p, const uint64_t (&acc)[NACC / 2], int ncol, int m0, int n,
-                                                  bool upper) {
-    const bool nv = n < p.N;
-    const int rows = nv ? min(ncol, p.M - m0) : 0;
-    const int64_t o = (int64_t)m0 * p.N + n;
-    __half* h = p.Y + o + (upper ? p.N : 0);
-    __half* pre = p.Z ? (upper ? p.U : p.Z) + o : nullptr;
-    const int odd = upper ? 1 : 0;
+__device__ __forceinline__ void fg_barrier(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Whether any of the warpgroup's threads has `bad` set.
+__device__ __forceinline__ bool fg_barrier_any(int id, bool bad) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"((uint32_t)bad)
+                 : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ uint2 half4(const float (&f)[4]) { return make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3])); }
+__device__ __forceinline__ void float4_of(const uint2& h, float (&f)[4]) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+
+// One tile's outputs.  acc: this thread's weight row (r of the CTA's 128) by ncol X rows from m0; nb:
+// the CTA's first output column; st: the warpgroup's staging rows; t: thread of the warpgroup.
+// Staged rows are [128 n] or, gated, [64 gate n | 64 up n with bit 4 flipped] (conflict-free stores).
+template <int ACT, bool GATED, int NACC>
+__device__ __forceinline__ void fg_epilogue(const FgArgs& p, const uint64_t (&acc)[NACC / 2], int ncol, int m0, int nb,
+                                            float* st, int r, int t, int bar) {
+    const int w = t >> 5, lane = t & 31;
+    const int col = GATED ? ((r & 16) ? 64 : 0) + (((r >> 5) * 16 + (r & 15)) ^ (r & 16)) : r;
+    const int n4 = GATED ? 4 * (lane & 15) : 4 * lane;  // this thread's four columns of the rows it finishes
+    const int n = nb + n4;
+    uint2 bias = make_uint2(0u, 0u);
+    if (!GATED && p.bias && n < p.N) bias = *reinterpret_cast<const uint2*>(p.bias + n);
 #pragma unroll
-    for (int c = 0; c < NACC; c += 2) {
-        if (c < ncol) {  // uniform over the warp
-            float v[2];
-            unpack_f32x2(acc[c / 2], v[0], v[1]);
-            const float other = __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
-            const float g = upper ? other : v[0], u = upper ? v[1] : other;
-            if (c + odd < rows) *h = __float2half_rn(act_fwd<ACT>(g) * u);
-            h += 2 * (int64_t)p.N;
-            if (pre) {
-                if (c < rows) *pre = __float2half_rn(v[0]);
-                if (c + 1 < rows) pre[p.N] = __float2half_rn(v[1]);
-                pre += 2 * (int64_t)p.N;
+    for (int c = 0; c < NACC; c += 32) {
+        if (c < ncol) {
+            const int rows = min(min(32, ncol - c), p.M - m0 - c);  // <= 0: nothing of this chunk exists
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float a, b;
+                unpack_f32x2(acc[(c + i) / 2], a, b);
+                st[i * 128 + col] = a;
+                st[(i + 1) * 128 + col] = b;
             }
+            fg_barrier(bar);
+            constexpr int RPW = GATED ? 2 : 1;  // rows a warp finishes at once
+            const int row0 = RPW * w + (GATED ? lane >> 4 : 0);
+            int64_t o = (int64_t)(m0 + c + row0) * p.N + n;
+            const float* sr = st + row0 * 128 + n4;
+#pragma unroll 1
+            for (int i = 0; i < 8 / RPW; i += 2) {  // two rows' residual loads in flight together
+                const int left = n < p.N ? rows - row0 - 4 * RPW * i : 0;
+                uint2 res[2];
+                if (!GATED && p.residual) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (4 * RPW * k < left)
+                            res[k] = *reinterpret_cast<const uint2*>(p.residual + o + (int64_t)(4 * RPW * k) * p.N);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (4 * RPW * k < left) {
+                        const float4 s0 = *reinterpret_cast<const float4*>(sr + 4 * RPW * k * 128);
+                        float z[4] = {s0.x, s0.y, s0.z, s0.w}, y[4];
+                        if constexpr (GATED) {
+                            const float4 s1 = *reinterpret_cast<const float4*>(sr + 4 * RPW * k * 128 + 64 + (n4 ^ 16) - n4);
+                            const float u[4] = {s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) y[j] = act_fwd<ACT>(z[j]) * u[j];
+                            if (p.U) *reinterpret_cast<uint2*>(p.U + o) = half4(u);
+                        } else {
+                            float f[4];
+                            float4_of(bias, f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                z[j] += f[j];
+                                y[j] = act_fwd<ACT>(z[j]);
+                            }
+                            if (p.residual) {
+                                float4_of(res[k], f);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) y[j] += f[j];
+                            }
+                        }
+                        *reinterpret_cast<uint2*>(p.Y + o) = half4(y);
+                        if (p.Z) *reinterpret_cast<uint2*>(p.Z + o) = half4(z);
+                    }
+                    o += (int64_t)(4 * RPW) * p.N;
+                }
+                sr += 8 * RPW * 128;
+            }
+            fg_barrier(bar);
         }
     }
 }
 
 template <bool GATED, int NMAX>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
                     const __grid_constant__ CUtensorMap tmW1, const FgArgs p) {
+    using C = FgCfg<NMAX>;
     constexpr int NACC = NMAX / 2;            // columns per fold thread
-    constexpr uint32_t TCOLS = NMAX > 64 ? 512 : 256;
-    constexpr uint32_t ACOL = 2 * NMAX;       // TMEM column of the first dequantised half group
-    constexpr bool SETREGS = NMAX > 64;
+    constexpr int NB = C::kNB, AG = C::kAG, GS = C::kDW / 2;
+    constexpr int FOLD_WARP = 4 + 4 * C::kDW;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_align1024(smem_raw);
     const uint32_t sbase = smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: the issuing loops stay in uniform registers
     const uint32_t rank = cluster_ctarank();
     const int S = p.stages;
     const uint32_t xbytes = (uint32_t)p.tn * 128u;  // tn/2 rows x 128 k x 2 bytes
     const uint32_t stage_bytes = xbytes + FG_P_BYTES;
-    auto x_addr = [&](int s) { return sbase + (uint32_t)s * stage_bytes; };
-    auto p_off = [&](int s) { return (uint32_t)s * stage_bytes + xbytes; };
-    const uint32_t bar0 = sbase + (uint32_t)S * stage_bytes;
+    const uint32_t epi0 = (uint32_t)S * stage_bytes;  // the epilogue's staging rows, then the barriers
+    const uint32_t bar0 = sbase + epi0 + 2 * FG_EPI;
     auto full_bar = [&](int s) { return bar0 + 8 * s; };
-    auto empty_bar = [&](int s) { return bar0 + 8 * (FG_MAXS + s); };
+    auto done_bar = [&](int s) { return bar0 + 8 * (FG_MAXS + s); };
     auto a_full = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + i); };
-    auto a_empty = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + FG_ASLOTS + i); };
-    auto d_full = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + 2 * FG_ASLOTS + i); };
-    auto d_empty = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + 2 * FG_ASLOTS + 2 + i); };
-    unsigned char* tail = smem + (uint32_t)S * stage_bytes + 8 * (2 * FG_MAXS + 2 * FG_ASLOTS + 4);
+    auto d_empty = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + 4 + i); };
+    unsigned char* tail = smem + epi0 + 2 * FG_EPI + 8 * (2 * FG_MAXS + 8);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1);
+            mbar_init(done_bar(s), 1);
         }
-        for (int i = 0; i < FG_ASLOTS; ++i) {
-            mbar_init(a_full(i), 8);   // four warps of each CTA
-            mbar_init(a_empty(i), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(d_full(i), 1);
-            mbar_init(d_empty(i), 16);  // eight warps of each CTA
-        }
+        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 16);   // eight warps of each CTA
+        for (int i = 0; i < NB; ++i) mbar_init(d_empty(i), 16);  // eight warps of each CTA
         *abort_flag = 0;
         fence_mbarrier_init();
         prefetch_tmap(&tmX);
@@ -242,14 +288,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
         if (GATED) prefetch_tmap(&tmW1);
     }
     if (warp == 2) {
-        tmem_alloc_pair(smem_u32(tmem_slot), TCOLS);
+        tmem_alloc_pair(smem_u32(tmem_slot), 512);
         tmem_relinquish_pair();
     }
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     pdl_launch_dependents();
 
     auto fail = [&]() {
@@ -259,11 +305,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
     const int cluster = (int)blockIdx.x >> 1, n_clusters = (int)gridDim.x >> 1;
 
     if (warp < 4) {
-        if (SETREGS) regs_dec<FG_REGS_MISC>();
-        if (warp == 0 && lane == 0) {
-            // -------------------------------------------------------- TMA producer
+        regs_dec<C::kRegsMisc>();
+        if (warp == 0) {
+            // -------------------------------------------------------- TMA producer (one lane issuing)
             auto load_w = [&](const FgUnit& u, int g, int s) {
-                const uint32_t dst = sbase + p_off(s);
+                const uint32_t dst = sbase + (uint32_t)s * stage_bytes + xbytes;
                 if constexpr (GATED) {
                     const int n = u.nt * 128 + (int)rank * 64;
 #pragma unroll
@@ -276,87 +322,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
                 }
             };
             if (!p.early) pdl_wait();
-            int it = 0, ahead = 0;
+            int ahead = 0;
             if (p.early) {  // the first ring's weights, before the preceding kernel has finished
                 for (int u = cluster; u < p.units && ahead < S; u += n_clusters) {
                     const FgUnit w = fg_unit(p, u);
                     for (int g = w.g0; g < w.g1 && ahead < S; ++g, ++ahead) {
-                        mbar_arrive_expect_tx(full_bar(ahead), stage_bytes);
-                        load_w(w, g, ahead);
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(full_bar(ahead), stage_bytes);
+                            load_w(w, g, ahead);
+                        }
+                        __syncwarp();
                     }
                 }
                 pdl_wait();
             }
+            int it = 0, s = 0;
+            uint32_t ph = 1;
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
                 const int mx = w.m0 + (int)rank * (p.tn / 2);
                 for (int g = w.g0; g < w.g1; ++g, ++it) {
-                    const int s = it % S;
-                    const uint32_t ph = (uint32_t)(it / S) & 1;
-                    if (it >= ahead) {
-                        if (!mbar_wait_cluster(empty_bar(s), ph ^ 1, abort_flag)) { fail(); ok = false; break; }
-                        mbar_arrive_expect_tx(full_bar(s), stage_bytes);
-                        load_w(w, g, s);
+                    if (it >= ahead && !mbar_wait_bounded(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
+                    if (elect_one()) {
+                        const uint32_t xs = sbase + (uint32_t)s * stage_bytes;
+                        if (it >= ahead) {
+                            mbar_arrive_expect_tx(full_bar(s), stage_bytes);
+                            load_w(w, g, s);
+                        }
+                        tma_load_2d(xs, &tmX, g * 128, mx, full_bar(s));
+                        tma_load_2d(xs + xbytes / 2, &tmX, g * 128 + 64, mx, full_bar(s));
                     }
-                    tma_load_2d(x_addr(s), &tmX, g * 128, mx, full_bar(s));
-                    tma_load_2d(x_addr(s) + xbytes / 2, &tmX, g * 128 + 64, mx, full_bar(s));
+                    __syncwarp();
+                    if (++s == S) { s = 0; ph ^= 1; }
                 }
             }
             // Never leave with loads in flight or with the tensor cores still to arrive on this CTA's
-            // barriers: wait (bounded) for the last use of every stage and of every dequantised slot.
+            // barriers: wait (bounded) for the last use of every stage.
             for (int i = max(it - S, 0); i < it; ++i) {
                 mbar_wait_bounded(full_bar(i % S), (uint32_t)(i / S) & 1, nullptr, 200000000ull);
-                if (ok) mbar_wait_cluster(empty_bar(i % S), (uint32_t)(i / S) & 1, abort_flag);
+                if (ok) mbar_wait_bounded(done_bar(i % S), (uint32_t)(i / S) & 1, abort_flag);
             }
-            for (int i = max(it - 2, 0); i < it && ok; ++i)
-                for (int h = 0; h < 2; ++h)
-                    mbar_wait_cluster(a_empty(2 * (i & 1) + h), (uint32_t)(i >> 1) & 1, abort_flag);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // -------------------------------------------------------- MMA issuer (for both CTAs)
             const uint32_t idesc = idesc_f16_f32(256, p.tn);
             pdl_wait();
-            int it = 0;
+            int it = 0, s = 0;
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
-                for (int g = w.g0; g < w.g1 && ok; ++g, ++it) {
-                    const int s = it % S, b = it & 1;
-                    const uint32_t ph = (uint32_t)(it >> 1) & 1;
-                    if (!mbar_wait_cluster(d_empty(b), ph ^ 1, abort_flag)) { fail(); ok = false; break; }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int a = 2 * b + h;
-                        if (!mbar_wait_cluster(a_full(a), ph, abort_flag)) { fail(); ok = false; break; }
-                        tc_fence_after();
-                        const uint64_t bd = sw128_kmajor_desc(x_addr(s) + h * (xbytes / 2));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_f16_ts_pair(tmem + b * NMAX, tmem + ACOL + a * 32 + j * 8, bd + 2 * j, idesc, (h | j) != 0);
-                        tc_commit_pair(a_empty(a));
+                for (int g = w.g0; g < w.g1; ++g, ++it) {
+                    const int b = it % NB, a = it % AG;
+                    if (!mbar_wait_bounded(d_empty(b), ((uint32_t)(it / NB) & 1) ^ 1, abort_flag) ||
+                        !mbar_wait_bounded(a_full(a), (uint32_t)(it / AG) & 1, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
                     }
-                    if (!ok) break;
-                    tc_commit_pair(empty_bar(s));
-                    tc_commit_pair(d_full(b));
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes);
+                        const uint64_t half = (uint64_t)(xbytes / 2) >> 4;  // the second 64 k
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mma_f16_ts_pair(tmem + b * NMAX, tmem + C::kACol + a * 64 + j * 8,
+                                            bd + (j >> 2) * half + 2 * (j & 3), idesc, j != 0);
+                        tc_commit_pair(done_bar(s));
+                    }
+                    __syncwarp();
+                    if (++s == S) s = 0;
                 }
             }
             // on an abort nobody else waits for what was issued: the pair's TMEM is freed after it
-            if (!ok && it > 0)
-                mbar_wait_cluster(d_full((it - 1) & 1), (uint32_t)((it - 1) >> 1) & 1, nullptr, 200000000ull);
+            if (!ok && it > 0) mbar_wait_bounded(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
         }
-    } else if (warp < 12) {
-        if (SETREGS) regs_dec<FG_REGS_DEQ>();
+    } else if (warp < FOLD_WARP) {
+        regs_dec<C::kRegsDeq>();
         // ------------------------------------------------------------ dequantisation
-        const int h = (warp - 4) >> 2, q = warp & 3;
+        const int wg = (warp - 4) >> 2, h = wg & 1, q = warp & 3;
         const int r = q * 32 + lane;  // row of the CTA's 128 = TMEM lane
         const uint32_t sw = (uint32_t)(r >> 1) & 3;  // 64-byte TMA swizzle
-        const uint32_t c0 = (uint32_t)r * 64 + (((2 * h) ^ sw) << 4), c1 = (uint32_t)r * 64 + (((2 * h + 1) ^ sw) << 4);
+        const uint32_t c0 = xbytes + (uint32_t)r * 64 + (((2 * h) ^ sw) << 4);
+        const uint32_t c1 = xbytes + (uint32_t)r * 64 + (((2 * h + 1) ^ sw) << 4);
         const uint8_t* zbase = GATED && lane >= 16 ? p.z1 : p.z0;
-        const uint32_t remote = map_shared(a_full(h), 0);  // slot h, then 2 + h
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + ACOL + (uint32_t)h * 32;
+        const uint32_t remote = map_shared(a_full(0), 0);
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol + (uint32_t)h * 32;
         pdl_wait();  // no bounded wait runs beside the preceding kernel
         bool ok = true;
-        int it = 0;
+        int it = 0, s = 0, sa = 0;  // ring stages of group it and of group it - AG
+        uint32_t ph = 0, pa = 0;
         for (int u = cluster; u < p.units; u += n_clusters) {
             const FgUnit w = fg_unit(p, u);
             const int n = GATED ? w.nt * 128 + (int)rank * 64 + 16 * q + (lane & 15) : w.nt * 256 + (int)rank * 128 + r;
@@ -365,19 +419,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
             uint32_t z4 = nv ? fg_zeros4(zrow, w.g0, p.G, p.vec) : 0;
             uint32_t z4n = 0;
             for (int g = w.g0; g < w.g1; ++g, ++it) {
-                const int s = it % S, b = it & 1;
                 // the next four groups' zero points are fetched while these four are used
                 if ((g & 3) == 0 && g > w.g0) z4 = z4n;
                 if (((g & 3) == 0 || g == w.g0) && nv && (g & ~3) + 4 < p.G) z4n = fg_zeros4(zrow, (g & ~3) + 4, p.G, p.vec);
+                const int cs = s, ca = sa;
+                const uint32_t cph = ph, cpa = pa;
+                if (++s == S) { s = 0; ph ^= 1; }
+                if (it >= AG && ++sa == S) { sa = 0; pa ^= 1; }
+                if (GS > 1 && (it % GS) != (wg >> 1)) continue;
                 const uint32_t z = (z4 >> (8 * (g & 3))) & 0xFFu;
                 // q - z = (1024 + q) - (1024 + z) from a low nibble, (1024 + 16 q) / 16 - (64 + z) from a
                 // high one: exact
                 const uint32_t zl = (0x6400u + z) * 0x10001u, zh = (0xD400u | (z << 4)) * 0x10001u;
-                if (ok && !mbar_wait_bounded(full_bar(s), (uint32_t)(it / S) & 1, abort_flag)) { fail(); ok = false; }
-                if (ok && !mbar_wait_cluster(a_empty(2 * b + h), ((uint32_t)(it >> 1) & 1) ^ 1, abort_flag)) { fail(); ok = false; }
+                if (ok && !mbar_wait_bounded(full_bar(cs), cph, abort_flag)) { fail(); ok = false; }
                 if (!ok) continue;
-                const uint4 wa = *reinterpret_cast<const uint4*>(smem + p_off(s) + c0);
-                const uint4 wb = *reinterpret_cast<const uint4*>(smem + p_off(s) + c1);
+                const unsigned char* st = smem + (uint32_t)cs * stage_bytes;
+                const uint4 wa = *reinterpret_cast<const uint4*>(st + c0);
+                const uint4 wb = *reinterpret_cast<const uint4*>(st + c1);
                 const uint32_t words[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
                 uint32_t o[32];
 #pragma unroll
@@ -392,26 +450,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
                     o[4 * c + 2] = __byte_perm(lo0, hi0, 0x7632);  // k4, k5
                     o[4 * c + 3] = __byte_perm(lo1, hi1, 0x7632);  // k6, k7
                 }
-                tmem_st_32x32b_x32(taddr + (uint32_t)b * 64, o);
+                // the group that used these columns AG groups ago has been multiplied
+                if (it >= AG && !mbar_wait_bounded(done_bar(ca), cpa, abort_flag)) { fail(); ok = false; continue; }
+                tmem_st_32x32b_x32(taddr + (uint32_t)(it % AG) * 64, o);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(remote + 16u * b);
+                if (lane == 0) mbar_arrive_cluster(remote + 8u * (uint32_t)(it % AG));
             }
         }
     } else {
-        if (SETREGS) regs_inc<FG_REGS_FOLD>();
+        regs_inc<C::kRegsFold>();
         // ------------------------------------------------------------ fold and epilogue
-        const int f = (warp - 12) >> 2, q = warp & 3;
+        const int f = (warp - FOLD_WARP) >> 2, q = warp & 3;
         const int r = q * 32 + lane;
         const int ncol = p.tn / 2;
         const bool upper = lane >= 16;
         const unsigned short* sbase_row = GATED && upper ? p.s1 : p.s0;
         const uint32_t remote = map_shared(d_empty(0), 0);
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(f * ncol);
+        float* st = reinterpret_cast<float*>(smem + epi0 + (uint32_t)f * FG_EPI);
         pdl_wait();  // the outputs may be read, the residual written, by the preceding kernel
         bool ok = true;
-        int it = 0;
+        int it = 0, s = 0;
+        uint32_t ph = 0;
         for (int u = cluster; u < p.units; u += n_clusters) {
             const FgUnit w = fg_unit(p, u);
             const int n = GATED ? w.nt * 128 + (int)rank * 64 + 16 * q + (lane & 15) : w.nt * 256 + (int)rank * 128 + r;
@@ -422,29 +484,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < NACC / 2; ++i) acc[i] = 0;
             for (int g = w.g0; g < w.g1; ++g, ++it) {
-                const int b = it & 1;
                 if ((g & 3) == 0 && g > w.g0) s4 = s4n;
                 if (((g & 3) == 0 || g == w.g0) && nv && (g & ~3) + 4 < p.G) s4n = fg_scales4(srow, (g & ~3) + 4, p.G, p.vec);
                 const float sc = __half2float(__ushort_as_half((unsigned short)(s4 >> (16 * (g & 3)))));
                 const uint64_t sc2 = pack_f32x2(__float_as_uint(sc), __float_as_uint(sc));
-                if (ok && !mbar_wait_cluster(d_full(b), (uint32_t)(it >> 1) & 1, abort_flag)) { fail(); ok = false; }
+                if (ok && !mbar_wait_bounded(done_bar(s), ph, abort_flag)) { fail(); ok = false; }
+                if (++s == S) { s = 0; ph ^= 1; }
                 if (!ok) continue;
                 tc_fence_after();
+                const uint32_t src = taddr + (uint32_t)(it % NB) * NMAX;
+                // rounds of 48 or 32 columns, each one wait (columns past tn hold old sums: never stored);
+                // 48 does not fit beside the plain epilogue's registers
+                constexpr int RC = NACC >= 48 && GATED ? 48 : 32;
 #pragma unroll
-                for (int c = 0; c < NACC; c += 16) {
+                for (int c = 0; c < NACC; c += RC) {
                     if (c < ncol) {
-                        uint32_t v[16];
-                        tmem_ld_32x32b_x16(taddr + (uint32_t)(b * NMAX + c), v);
+                        uint32_t v[RC / 16][16];
+#pragma unroll
+                        for (int k = 0; k < RC / 16; ++k) tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[k]);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) fma2(acc[(c + i) / 2], pack_f32x2(v[i], v[i + 1]), sc2);
+                        for (int k = 0; k < RC / 16; ++k) {
+                            fg_tie(v[k]);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) fma2(acc[(c + 16 * k + i) / 2], pack_f32x2(v[k][i], v[k][i + 1]), sc2);
+                        }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(remote + 8u * b);
+                if (lane == 0) mbar_arrive_cluster(remote + 8u * (uint32_t)(it % NB));
             }
-            if (!ok) continue;
+            if (fg_barrier_any(1 + f, !ok)) continue;  // all four warps agree before the staging barriers
             const int m0 = w.m0 + f * ncol;
             if (p.P) {
                 float* P = p.P + ((int64_t)w.slice * (GATED ? 2 : 1) + (GATED && upper ? 1 : 0)) * p.M * p.N;
@@ -456,12 +527,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
                     if (c < ncol && nv && m0 + c + 1 < p.M) P[(int64_t)(m0 + c + 1) * p.N + n] = v[1];
                 }
             } else {
-                auto epilogue = [&](auto act) {
-                    if constexpr (GATED) fg_epilogue_gated<decltype(act)::value, NACC>(p, acc, ncol, m0, n, upper);
-                    else fg_epilogue_plain<decltype(act)::value, NACC>(p, acc, ncol, m0, n);
+                const int nb = GATED ? w.nt * 128 + (int)rank * 64 : w.nt * 256 + (int)rank * 128;
+                dispatch_act(p.act, [&](auto act) {
+                    fg_epilogue<decltype(act)::value, GATED, NACC>(p, acc, ncol, m0, nb, st, r, r, 1 + f);
                     return cudaSuccess;
-                };
-                dispatch_act(p.act, epilogue);
+                });
             }
         }
     }
@@ -469,7 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FG_THREADS, 1)
     cluster_sync();  // nothing of the pair's products or arrivals is outstanding in either CTA
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, TCOLS);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -558,8 +628,8 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
     }
     best.wide = best.tn > 64;
     const uint32_t stage = (uint32_t)best.tn * 128u + FG_P_BYTES;
-    best.stages = (int)std::min<uint32_t>((FG_SMEM - 1024 - 512) / stage, FG_MAXS);
-    best.smem = stage * (uint32_t)best.stages + 512 + 1024;
+    best.stages = (int)std::min<uint32_t>((FG_SMEM - 1024 - 512 - 2 * FG_EPI) / stage, FG_MAXS);
+    best.smem = stage * (uint32_t)best.stages + 2 * FG_EPI + 512 + 1024;
     return best;
 }
 
@@ -576,7 +646,7 @@ cudaError_t fg_setup() {
         // the register split must add up to the launch's allotment, or setmaxnreg.inc would wait for good
         cudaFuncAttributes a;
         if (err[dev] == cudaSuccess) err[dev] = cudaFuncGetAttributes(&a, ffn_gemm_kernel<GATED, NMAX>);
-        if (err[dev] == cudaSuccess && NMAX > 64 && a.numRegs != FG_REGS_LAUNCH) err[dev] = cudaErrorInvalidConfiguration;
+        if (err[dev] == cudaSuccess && a.numRegs != FgCfg<NMAX>::kRegs) err[dev] = cudaErrorInvalidConfiguration;
     });
     return err[dev];
 }
@@ -588,7 +658,7 @@ cudaError_t fg_launch(const CUtensorMap& tx, const CUtensorMap& t0, const CUtens
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * std::min(pl.units, std::max(1, device_sm_count() / 2))), 1, 1);
-    cfg.blockDim = dim3(FG_THREADS, 1, 1);
+    cfg.blockDim = dim3(FgCfg<NMAX>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -218,6 +218,15 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
            | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
 
+// One lane of a converged warp.  A loop that the whole warp runs, with the tcgen05 and TMA
+// instructions behind this predicate, keeps their operands in uniform registers; behind
+// `lane == 0` every instruction pays for moving its operands there (67 cycles for each MMA and commit).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // ------------------------------------------------------------------ CTA pairs (clusters of two)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
@@ -237,28 +246,11 @@ __device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank) {
     return r;
 }
 
-// Arrive on an mbarrier of either CTA (address from map_shared), releasing to the cluster.
+// Arrive on an mbarrier of either CTA (address from map_shared).  What the arrival hands over lies in
+// tensor memory or was written by TMA (ordered by tcgen05 fences and the barriers' own phases), so no
+// cluster-scope fence of generic memory goes with it: that would flush and invalidate L1 every time.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// mbar_wait_bounded for barriers that the other CTA's threads arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
-                                                  uint64_t limit_ns = 2000000000ull) {
-    uint64_t t0 = 0;
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(1000u)
-            : "memory");
-        if (ok) return true;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0) t0 = t;
-        if ((abort && *abort) || t - t0 > limit_ns) return false;
-    }
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
