@@ -19,8 +19,7 @@
 //   warp 0       TMA producer of its CTA: per group X (two boxes of 64 k) and the packed rows
 //   warp 1       CTA 0: issues the pair's tcgen05.mma (M = 256, N = tn, K = 16) and one commit a group
 //   warp 2       TMEM allocation
-//   next 4 DW    dequantise: 4 warps take a group's k 0-63, 4 its k 64-127 (a row's 64 codes -> 32 TMEM
-//                columns); with DW = 4 two such pairs alternate between groups
+//   next 4 DW    dequantise: DW warpgroups take the groups in turn (a row's 128 codes -> 64 TMEM columns)
 //   last 8       fold: four take columns 0 .. tn/2 - 1, four the rest: read a group's sums from TMEM,
 //                acc += s * sum in registers; after the last group the epilogue
 // The group sums rotate through NB TMEM buffers, the dequantised groups through AG, so a group's
@@ -61,6 +60,7 @@ constexpr uint32_t FG_EPI = 32 * 128 * 4;          // a fold warpgroup's 32 rows
 template <int NMAX>
 struct FgCfg {
     static constexpr bool kWide = NMAX > 64;
+    static constexpr int kSubs = kWide ? 2 : 1;     // products a group is issued as (tn / kSubs columns each)
     static constexpr int kDW = kWide ? 2 : 4;       // dequantising warpgroups
     static constexpr int kNB = kWide ? 2 : 4;       // TMEM buffers of group sums
     static constexpr int kAG = kWide ? 2 : 4;       // dequantised groups in TMEM (64 columns each)
@@ -94,6 +94,11 @@ struct FgArgs {
     int* status;
 };
 
+// A bounded wait by a whole warp, with one outcome for it (what follows is warp-synchronous).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
+}
+
 struct FgUnit {
     int m0, nt, slice, g0, g1;
 };
@@ -108,8 +113,8 @@ __device__ __forceinline__ FgUnit fg_unit(const FgArgs& p, int u) {
     const int rem = t - grp * per;
     r.m0 = (first + rem % gm) * p.tn;
     r.nt = rem / gm;
-    r.g0 = (int)((int64_t)r.slice * p.G / p.ks);
-    r.g1 = (int)((int64_t)(r.slice + 1) * p.G / p.ks);
+    r.g0 = r.slice * p.G / p.ks;  // G < 2^24, ks <= 16
+    r.g1 = (r.slice + 1) * p.G / p.ks;
     return r;
 }
 
@@ -173,12 +178,16 @@ __device__ __forceinline__ void float4_of(const uint2& h, float (&f)[4]) {
 }
 
 // One tile's outputs.  acc: this thread's weight row (r of the CTA's 128) by ncol X rows from m0; nb:
-// the CTA's first output column; st: the warpgroup's staging rows; t: thread of the warpgroup.
+// the CTA's first output column; st_off: the warpgroup's staging rows.
 // Staged rows are [128 n] or, gated, [64 gate n | 64 up n with bit 4 flipped] (conflict-free stores).
 template <int ACT, bool GATED, int NACC>
 __device__ __forceinline__ void fg_epilogue(const FgArgs& p, const uint64_t (&acc)[NACC / 2], int ncol, int m0, int nb,
-                                            float* st, int r, int t, int bar) {
-    const int w = t >> 5, lane = t & 31;
+                                            unsigned char* smem, uint32_t st_off, int r, int bar) {
+    // opaque to the compiler: what follows from it is computed here, once a tile, and not kept in
+    // registers (or spilled) across the group loop
+    asm volatile("" : "+r"(r), "+r"(st_off));
+    float* st = reinterpret_cast<float*>(smem + st_off);
+    const int w = r >> 5, lane = r & 31;
     const int col = GATED ? ((r & 16) ? 64 : 0) + (((r >> 5) * 16 + (r & 15)) ^ (r & 16)) : r;
     const int n4 = GATED ? 4 * (lane & 15) : 4 * lane;  // this thread's four columns of the rows it finishes
     const int n = nb + n4;
@@ -253,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     const __grid_constant__ CUtensorMap tmW1, const FgArgs p) {
     using C = FgCfg<NMAX>;
     constexpr int NACC = NMAX / 2;            // columns per fold thread
-    constexpr int NB = C::kNB, AG = C::kAG, GS = C::kDW / 2;
+    constexpr int NB = C::kNB, AG = C::kAG, GS = C::kDW, SUBS = C::kSubs;
     constexpr int FOLD_WARP = 4 + 4 * C::kDW;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_align1024(smem_raw);
@@ -270,17 +279,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
     auto done_bar = [&](int s) { return bar0 + 8 * (FG_MAXS + s); };
     auto a_full = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + i); };
     auto d_empty = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + 4 + i); };
-    unsigned char* tail = smem + epi0 + 2 * FG_EPI + 8 * (2 * FG_MAXS + 8);
+    auto d_full = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + 8 + i); };
+    unsigned char* tail = smem + epi0 + 2 * FG_EPI + 8 * (2 * FG_MAXS + 12);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(done_bar(s), 1);
+            mbar_init(done_bar(s), SUBS);
         }
-        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 16);   // eight warps of each CTA
-        for (int i = 0; i < NB; ++i) mbar_init(d_empty(i), 16);  // eight warps of each CTA
+        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 8);    // a dequantising warpgroup of each CTA
+        for (int i = 0; i < SUBS * NB; ++i) {
+            mbar_init(d_empty(i), 16 / SUBS);  // eight warps of each CTA, or the four that fold this product
+            mbar_init(d_full(i), 1);
+        }
         *abort_flag = 0;
         fence_mbarrier_init();
         prefetch_tmap(&tmX);
@@ -341,7 +354,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
-                const int mx = w.m0 + (int)rank * (p.tn / 2);
+                const int part = p.tn / (2 * SUBS);  // X rows of one product in this CTA
+                const int mx = w.m0 + (int)rank * part;
                 for (int g = w.g0; g < w.g1; ++g, ++it) {
                     if (it >= ahead && !mbar_wait_bounded(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
                     if (elect_one()) {
@@ -350,8 +364,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                             mbar_arrive_expect_tx(full_bar(s), stage_bytes);
                             load_w(w, g, s);
                         }
-                        tma_load_2d(xs, &tmX, g * 128, mx, full_bar(s));
-                        tma_load_2d(xs + xbytes / 2, &tmX, g * 128 + 64, mx, full_bar(s));
+#pragma unroll
+                        for (int f = 0; f < SUBS; ++f) {
+                            const uint32_t xf = xs + (uint32_t)f * (xbytes / 4);
+                            tma_load_2d(xf, &tmX, g * 128, mx + 2 * f * part, full_bar(s));
+                            tma_load_2d(xf + xbytes / 2, &tmX, g * 128 + 64, mx + 2 * f * part, full_bar(s));
+                        }
                     }
                     __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
@@ -363,16 +381,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 mbar_wait_bounded(full_bar(i % S), (uint32_t)(i / S) & 1, nullptr, 200000000ull);
                 if (ok) mbar_wait_bounded(done_bar(i % S), (uint32_t)(i / S) & 1, abort_flag);
             }
-        } else if (warp == 1 && rank == 0) {
-            // -------------------------------------------------------- MMA issuer (for both CTAs)
-            const uint32_t idesc = idesc_f16_f32(256, p.tn);
+        } else if ((warp == 1 || (SUBS == 2 && warp == 3)) && rank == 0) {
+            // -------------------------------------------------------- MMA issuers (for both CTAs)
+            const int f = SUBS == 2 ? warp >> 1 : 0;  // which of the group's products
+            const uint32_t idesc = idesc_f16_f32(256, p.tn / SUBS);
             pdl_wait();
             int it = 0, s = 0;
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
                 for (int g = w.g0; g < w.g1; ++g, ++it) {
-                    const int b = it % NB, a = it % AG;
+                    const int b = f * NB + it % NB, a = it % AG;
                     if (!mbar_wait_bounded(d_empty(b), ((uint32_t)(it / NB) & 1) ^ 1, abort_flag) ||
                         !mbar_wait_bounded(a_full(a), (uint32_t)(it / AG) & 1, abort_flag)) {
                         fail();
@@ -381,12 +400,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     }
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes);
+                        const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes + (uint32_t)f * (xbytes / 4));
                         const uint64_t half = (uint64_t)(xbytes / 2) >> 4;  // the second 64 k
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            mma_f16_ts_pair(tmem + b * NMAX, tmem + C::kACol + a * 64 + j * 8,
+                            mma_f16_ts_pair(tmem + b * (NMAX / SUBS), tmem + C::kACol + a * 64 + j * 8,
                                             bd + (j >> 2) * half + 2 * (j & 3), idesc, j != 0);
+                        if (SUBS == 2) tc_commit_pair(d_full(b));
                         tc_commit_pair(done_bar(s));
                     }
                     __syncwarp();
@@ -394,70 +414,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 }
             }
             // on an abort nobody else waits for what was issued: the pair's TMEM is freed after it
-            if (!ok && it > 0) mbar_wait_bounded(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
+            if (!ok && it > 0 && SUBS == 1)
+                mbar_wait_bounded(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
+            if (!ok && it > 0 && SUBS == 2)
+                mbar_wait_bounded(d_full(f * NB + (it - 1) % NB), (uint32_t)((it - 1) / NB) & 1, nullptr, 200000000ull);
         }
     } else if (warp < FOLD_WARP) {
         regs_dec<C::kRegsDeq>();
         // ------------------------------------------------------------ dequantisation
-        const int wg = (warp - 4) >> 2, h = wg & 1, q = warp & 3;
+        static_assert(GS == AG, "each warpgroup has its own slot");
+        const int wg = (warp - 4) >> 2, q = warp & 3;  // this warpgroup's groups: wg, wg + GS, ...
         const int r = q * 32 + lane;  // row of the CTA's 128 = TMEM lane
         const uint32_t sw = (uint32_t)(r >> 1) & 3;  // 64-byte TMA swizzle
-        const uint32_t c0 = xbytes + (uint32_t)r * 64 + (((2 * h) ^ sw) << 4);
-        const uint32_t c1 = xbytes + (uint32_t)r * 64 + (((2 * h + 1) ^ sw) << 4);
+        const uint32_t c0 = xbytes + (uint32_t)r * 64;
         const uint8_t* zbase = GATED && lane >= 16 ? p.z1 : p.z0;
         const uint32_t remote = map_shared(a_full(0), 0);
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol + (uint32_t)h * 32;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol;
         pdl_wait();  // no bounded wait runs beside the preceding kernel
         bool ok = true;
-        int it = 0, s = 0, sa = 0;  // ring stages of group it and of group it - AG
+        int it = wg, s = wg, sa = wg;  // group, its ring stage, the ring stage of group it - AG (S >= GS, AG)
         uint32_t ph = 0, pa = 0;
+        // two of the row's four 16-byte pieces: half h of the group's codes
+        auto load = [&](int h, uint4& wa, uint4& wb) {
+            const unsigned char* st = smem + (uint32_t)s * stage_bytes + c0;
+            wa = *reinterpret_cast<const uint4*>(st + (((2 * h) ^ sw) << 4));
+            wb = *reinterpret_cast<const uint4*>(st + (((2 * h + 1) ^ sw) << 4));
+        };
+        int skip = wg;        // groups of the next unit that are not this warpgroup's
+        bool loaded = false;  // the first half of group it's codes is in wa, wb already
+        uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
         for (int u = cluster; u < p.units; u += n_clusters) {
             const FgUnit w = fg_unit(p, u);
             const int n = GATED ? w.nt * 128 + (int)rank * 64 + 16 * q + (lane & 15) : w.nt * 256 + (int)rank * 128 + r;
             const bool nv = n < p.N;
             const uint8_t* zrow = zbase + (int64_t)(nv ? n : 0) * p.G;
-            uint32_t z4 = nv ? fg_zeros4(zrow, w.g0, p.G, p.vec) : 0;
-            uint32_t z4n = 0;
-            for (int g = w.g0; g < w.g1; ++g, ++it) {
-                // the next four groups' zero points are fetched while these four are used
-                if ((g & 3) == 0 && g > w.g0) z4 = z4n;
-                if (((g & 3) == 0 || g == w.g0) && nv && (g & ~3) + 4 < p.G) z4n = fg_zeros4(zrow, (g & ~3) + 4, p.G, p.vec);
-                const int cs = s, ca = sa;
-                const uint32_t cph = ph, cpa = pa;
-                if (++s == S) { s = 0; ph ^= 1; }
-                if (it >= AG && ++sa == S) { sa = 0; pa ^= 1; }
-                if (GS > 1 && (it % GS) != (wg >> 1)) continue;
+            int g = w.g0 + skip;
+            uint32_t z4 = nv && g < w.g1 ? fg_zeros4(zrow, g, p.G, p.vec) : 0, z4n = 0;
+            int zb = g & ~3;  // z4 holds groups zb ... zb + 3, z4n the next four
+            if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
+            for (; g < w.g1; g += GS) {
+                if ((g & ~3) != zb) {  // the next four groups' zero points are fetched while these are used
+                    z4 = z4n;
+                    zb = g & ~3;
+                    if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
+                }
                 const uint32_t z = (z4 >> (8 * (g & 3))) & 0xFFu;
                 // q - z = (1024 + q) - (1024 + z) from a low nibble, (1024 + 16 q) / 16 - (64 + z) from a
                 // high one: exact
                 const uint32_t zl = (0x6400u + z) * 0x10001u, zh = (0xD400u | (z << 4)) * 0x10001u;
-                if (ok && !mbar_wait_bounded(full_bar(cs), cph, abort_flag)) { fail(); ok = false; }
-                if (!ok) continue;
-                const unsigned char* st = smem + (uint32_t)cs * stage_bytes;
-                const uint4 wa = *reinterpret_cast<const uint4*>(st + c0);
-                const uint4 wb = *reinterpret_cast<const uint4*>(st + c1);
-                const uint32_t words[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-                uint32_t o[32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t wd = words[c], w8 = wd >> 8;
-                    const uint32_t lo0 = hsub2_u32(lop3_and_or(wd, 0x000F000Fu, 0x64006400u), zl);              // k0, k4
-                    const uint32_t hi0 = hfma2_u32(lop3_and_or(wd, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k1, k5
-                    const uint32_t lo1 = hsub2_u32(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), zl);              // k2, k6
-                    const uint32_t hi1 = hfma2_u32(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k3, k7
-                    o[4 * c + 0] = __byte_perm(lo0, hi0, 0x5410);  // k0, k1
-                    o[4 * c + 1] = __byte_perm(lo1, hi1, 0x5410);  // k2, k3
-                    o[4 * c + 2] = __byte_perm(lo0, hi0, 0x7632);  // k4, k5
-                    o[4 * c + 3] = __byte_perm(lo1, hi1, 0x7632);  // k6, k7
+                if (!loaded) {
+                    if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
+                    load(0, wa, wb);
                 }
-                // the group that used these columns AG groups ago has been multiplied
-                if (it >= AG && !mbar_wait_bounded(done_bar(ca), cpa, abort_flag)) { fail(); ok = false; continue; }
-                tmem_st_32x32b_x32(taddr + (uint32_t)(it % AG) * 64, o);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(remote + 8u * (uint32_t)(it % AG));
+                loaded = false;
+                const uint32_t slot = (uint32_t)(it % AG);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t words[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                    uint32_t o[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t wd = words[c], w8 = wd >> 8;
+                        const uint32_t lo0 = hsub2_u32(lop3_and_or(wd, 0x000F000Fu, 0x64006400u), zl);              // k0, k4
+                        const uint32_t hi0 = hfma2_u32(lop3_and_or(wd, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k1, k5
+                        const uint32_t lo1 = hsub2_u32(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), zl);              // k2, k6
+                        const uint32_t hi1 = hfma2_u32(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k3, k7
+                        o[4 * c + 0] = __byte_perm(lo0, hi0, 0x5410);  // k0, k1
+                        o[4 * c + 1] = __byte_perm(lo1, hi1, 0x5410);  // k2, k3
+                        o[4 * c + 2] = __byte_perm(lo0, hi0, 0x7632);  // k4, k5
+                        o[4 * c + 3] = __byte_perm(lo1, hi1, 0x7632);  // k6, k7
+                    }
+                    if (h == 0) {
+                        load(1, wa, wb);
+                        if (it >= AG) {  // the group that used these columns AG groups ago has been multiplied
+                            if (ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
+                            sa += GS;
+                            if (sa >= S) { sa -= S; pa ^= 1; }
+                        }
+                    }
+                    if (ok) tmem_st_32x32b_x32(taddr + slot * 64 + h * 32, o);
+                }
+                it += GS;
+                s += GS;
+                if (s >= S) { s -= S; ph ^= 1; }
+                // the next group's codes, where they have arrived, are read while this one's are stored
+                if (ok && g + GS < w.g1 && __all_sync(0xffffffffu, mbar_test(full_bar(s), ph))) {
+                    load(0, wa, wb);
+                    loaded = true;
+                }
+                if (ok) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(remote + 8u * slot);
+                }
             }
+            skip = g - w.g1;
         }
     } else {
         regs_inc<C::kRegsFold>();
@@ -467,12 +519,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
         const int ncol = p.tn / 2;
         const bool upper = lane >= 16;
         const unsigned short* sbase_row = GATED && upper ? p.s1 : p.s0;
-        const uint32_t remote = map_shared(d_empty(0), 0);
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(f * ncol);
-        float* st = reinterpret_cast<float*>(smem + epi0 + (uint32_t)f * FG_EPI);
+        const uint32_t remote = map_shared(d_empty(SUBS == 2 ? f * NB : 0), 0);
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(SUBS == 2 ? f * NB * NACC : f * ncol);
         pdl_wait();  // the outputs may be read, the residual written, by the preceding kernel
         bool ok = true;
-        int it = 0, s = 0;
+        int b = 0, s = 0;  // TMEM buffer and, with one product a group, ring stage of the group
         uint32_t ph = 0;
         for (int u = cluster; u < p.units; u += n_clusters) {
             const FgUnit w = fg_unit(p, u);
@@ -483,37 +534,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             uint64_t acc[NACC / 2];
 #pragma unroll
             for (int i = 0; i < NACC / 2; ++i) acc[i] = 0;
-            for (int g = w.g0; g < w.g1; ++g, ++it) {
+            for (int g = w.g0; g < w.g1; ++g) {
                 if ((g & 3) == 0 && g > w.g0) s4 = s4n;
                 if (((g & 3) == 0 || g == w.g0) && nv && (g & ~3) + 4 < p.G) s4n = fg_scales4(srow, (g & ~3) + 4, p.G, p.vec);
                 const float sc = __half2float(__ushort_as_half((unsigned short)(s4 >> (16 * (g & 3)))));
                 const uint64_t sc2 = pack_f32x2(__float_as_uint(sc), __float_as_uint(sc));
-                if (ok && !mbar_wait_bounded(done_bar(s), ph, abort_flag)) { fail(); ok = false; }
-                if (++s == S) { s = 0; ph ^= 1; }
-                if (!ok) continue;
-                tc_fence_after();
-                const uint32_t src = taddr + (uint32_t)(it % NB) * NMAX;
-                // rounds of 48 or 32 columns, each one wait (columns past tn hold old sums: never stored);
-                // 48 does not fit beside the plain epilogue's registers
-                constexpr int RC = NACC >= 48 && GATED ? 48 : 32;
+                if (ok && !warp_wait(SUBS == 2 ? d_full(f * NB + b) : done_bar(s), ph, abort_flag)) { fail(); ok = false; }
+                if (SUBS == 1 && ++s == S) { s = 0; ph ^= 1; }
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t src = taddr + (uint32_t)(b * (SUBS == 2 ? NACC : NMAX));
+                    // rounds of 48 or 32 columns, each one wait (columns past tn hold old sums: never stored)
+                    constexpr int RC = NACC >= 48 && GATED ? 48 : 32;
 #pragma unroll
-                for (int c = 0; c < NACC; c += RC) {
-                    if (c < ncol) {
-                        uint32_t v[RC / 16][16];
+                    for (int c = 0; c < NACC; c += RC) {
+                        if (c < ncol) {
+                            uint32_t v[RC / 16][16];
 #pragma unroll
-                        for (int k = 0; k < RC / 16; ++k) tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[k]);
-                        tmem_wait_ld();
+                            for (int k = 0; k < RC / 16; ++k) tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[k]);
+                            tmem_wait_ld();
+                            if (c + RC >= ncol) {  // all read: the buffer is free
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive_cluster(remote + 8u * (uint32_t)b);
+                            }
 #pragma unroll
-                        for (int k = 0; k < RC / 16; ++k) {
-                            fg_tie(v[k]);
+                            for (int k = 0; k < RC / 16; ++k) {
+                                fg_tie(v[k]);
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) fma2(acc[(c + 16 * k + i) / 2], pack_f32x2(v[k][i], v[k][i + 1]), sc2);
+                                for (int i = 0; i < 16; i += 2)
+                                    fma2(acc[(c + 16 * k + i) / 2], pack_f32x2(v[k][i], v[k][i + 1]), sc2);
+                            }
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(remote + 8u * (uint32_t)(it % NB));
+                if (++b == NB) {
+                    b = 0;
+                    if (SUBS == 2) ph ^= 1;
+                }
             }
             if (fg_barrier_any(1 + f, !ok)) continue;  // all four warps agree before the staging barriers
             const int m0 = w.m0 + f * ncol;
@@ -529,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             } else {
                 const int nb = GATED ? w.nt * 128 + (int)rank * 64 : w.nt * 256 + (int)rank * 128;
                 dispatch_act(p.act, [&](auto act) {
-                    fg_epilogue<decltype(act)::value, GATED, NACC>(p, acc, ncol, m0, nb, st, r, r, 1 + f);
+                    fg_epilogue<decltype(act)::value, GATED, NACC>(p, acc, ncol, m0, nb, smem, epi0 + (uint32_t)f * FG_EPI, r, 1 + f);
                     return cudaSuccess;
                 });
             }
@@ -603,8 +661,8 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
     const int64_t n_tiles = (N + rows - 1) / rows;
     FgPlan best = {};
     double best_t = -1.0;
-    for (int tn = 32; tn <= 192; tn += 32) {
-        if (tn > 32 && tn >= M + 32) break;
+    for (int tn : {32, 64, 128, 192}) {
+        if (tn > 32 && tn / 2 >= M) break;
         const int64_t m_tiles = (M + tn - 1) / tn;
         const int64_t tiles = m_tiles * n_tiles;
         for (int ks = 1; ks <= 16 && ks <= G; ++ks) {
@@ -705,7 +763,8 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
     const FgPlan pl = fg_plan(M, N, K, gated);
     if (pl.ks > 1 && !ws) return cudaErrorInvalidValue;
     CUtensorMap tx, t0, t1;
-    if (!make_tensor_map_2d(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)K, (uint64_t)M, 64, (uint32_t)(pl.tn / 2),
+    if (!make_tensor_map_2d(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)K, (uint64_t)M, 64,
+                            (uint32_t)(pl.wide ? pl.tn / 4 : pl.tn / 2),
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     const uint32_t box = gated ? 16 : 128;
