@@ -11,6 +11,10 @@ the normal range).  Before that, a product's fp32 sum is off by
     below the same 2^-9 rms.
 
 So a product z is within E = 2^-9 rms(z), and what follows carries E through its derivatives.  The
+activations and their derivatives themselves are evaluated in fp32 to an absolute error of at most 2^-20
+where they are of order one (the normal tail's fit: 6.4e-7 of Phi <= 1; exponential, division and the
+multiply-adds behind them: a few 2^-24), which adds A = 2^-20 |factor|: it matters next to a derivative's
+zero, where E times the derivative vanishes and the rounding alone may use all of its half step.  The
 error's 2-norm is held to 2^-11 of the result's: fp16 rounding alone has 2^-11 / sqrt(3) / 1.36 = 2.1e-4,
 the rest at most the same again (gate: two factors)."""
 import numpy as np
@@ -25,6 +29,7 @@ from weight_only_int4_06_b200 import w4a16 as B
 pytestmark = pytest.mark.gpu
 
 E = 2.0 ** -9
+A = 2.0 ** -20
 HALF = 2.0 ** -11
 
 
@@ -169,8 +174,8 @@ def dx_gated_case(M, N, K, act, in_place=False, seed=61):
     e = E * rms(dH)
     U64, G64 = U.astype(np.float64), G.astype(np.float64)
     what = f"dx_gated {M}x{N}x{K} {act}"
-    check(dG, rG, e * np.abs(U64 * F.act_grad(G64, act)), what + " dG")
-    check(dU, rU, e * np.abs(F.act(G64, act)), what + " dU")
+    check(dG, rG, e * np.abs(U64 * F.act_grad(G64, act)) + A * np.abs(dH * U64), what + " dG")
+    check(dU, rU, e * np.abs(F.act(G64, act)) + A * np.abs(rU), what + " dU")
 
 
 @pytest.mark.parametrize("M,N,K", DX_SHAPES)

@@ -648,7 +648,7 @@ w4_status w4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int n_layer
     if (n_layers != 1 && n_layers != 2) return W4_ERR_UNSUPPORTED;
     const w4_status st = ffn_shape(M, N, K, group);
     if (st != W4_OK) return st;
-    *bytes = 0;
+    *bytes = M > 0 && N > 0 && K > 0 ? ffn_dx_workspace(M, N, K, n_layers) : 0;
     return W4_OK;
 }
 
@@ -671,7 +671,7 @@ w4_status w4_gemm_dx(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const 
     if (!status) return W4_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     if (N == 0) return zero_half(dX, M, K, s) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
-    const cudaError_t e = launch_dx_simple(dY, w, dY2, two ? &w2 : nullptr, M, N, K, nullptr, dX, s);
+    const cudaError_t e = launch_ffn_dx(dY, w, dY2, two ? &w2 : nullptr, M, N, K, nullptr, dX, ws, status, s);
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
@@ -696,7 +696,7 @@ w4_status w4_gemm_dx_gated(const uint16_t* dY, int64_t M, int64_t N, int64_t K, 
     if (N == 0)
         return zero_half(dG, M, K, s) == cudaSuccess && zero_half(dU, M, K, s) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
     const W4GateGrad gate = {G, U, activation, dG, dU};
-    const cudaError_t e = launch_dx_simple(dY, w, nullptr, nullptr, M, N, K, &gate, nullptr, s);
+    const cudaError_t e = launch_ffn_dx(dY, w, nullptr, nullptr, M, N, K, &gate, nullptr, ws, status, s);
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 

@@ -41,6 +41,7 @@
 #include <mutex>
 
 #include "activation.cuh"
+#include "ffn_common.cuh"
 #include "internal.h"
 #include "sm100.cuh"
 
@@ -85,36 +86,26 @@ struct FgArgs {
     int act;
     int M, N, G;
     int tn;           // X rows per tile
-    int m_tiles, n_tiles, gm;  // raster: gm m-tiles run down the n-tiles together
-    int ks;           // K slices
-    int units;        // m_tiles * n_tiles * ks
+    FfnRaster raster;  // ks: slices of K
+    int units;
     int stages;
     int vec;          // metadata rows allow 4-group vector loads
     int early;        // weights may be read before the preceding kernel has finished
     int* status;
 };
 
-// A bounded wait by a whole warp, with one outcome for it (what follows is warp-synchronous).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
-}
-
 struct FgUnit {
     int m0, nt, slice, g0, g1;
 };
 
 __device__ __forceinline__ FgUnit fg_unit(const FgArgs& p, int u) {
+    const FfnUnit t = ffn_unit(p.raster, u);
     FgUnit r;
-    r.slice = u % p.ks;
-    const int t = u / p.ks;
-    const int per = p.gm * p.n_tiles;
-    const int grp = t / per, first = grp * p.gm;
-    const int gm = min(p.gm, p.m_tiles - first);
-    const int rem = t - grp * per;
-    r.m0 = (first + rem % gm) * p.tn;
-    r.nt = rem / gm;
-    r.g0 = r.slice * p.G / p.ks;  // G < 2^24, ks <= 16
-    r.g1 = (r.slice + 1) * p.G / p.ks;
+    r.slice = t.slice;
+    r.nt = t.nt;
+    r.m0 = t.mt * p.tn;
+    r.g0 = t.slice * p.G / p.raster.ks;  // G < 2^24, ks <= 16
+    r.g1 = (t.slice + 1) * p.G / p.raster.ks;
     return r;
 }
 
@@ -157,26 +148,6 @@ __device__ __forceinline__ void fg_tie(uint32_t (&v)[16]) {
                       "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
 }
 
-__device__ __forceinline__ void fg_barrier(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-
-// Whether any of the warpgroup's threads has `bad` set.
-__device__ __forceinline__ bool fg_barrier_any(int id, bool bad) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 128, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"(id), "r"((uint32_t)bad)
-                 : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ uint2 half4(const float (&f)[4]) { return make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3])); }
-__device__ __forceinline__ void float4_of(const uint2& h, float (&f)[4]) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
-    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
-}
-
 // One tile's outputs.  acc: this thread's weight row (r of the CTA's 128) by ncol X rows from m0; nb:
 // the CTA's first output column; st_off: the warpgroup's staging rows.
 // Staged rows are [128 n] or, gated, [64 gate n | 64 up n with bit 4 flipped] (conflict-free stores).
@@ -204,7 +175,7 @@ __device__ __forceinline__ void fg_epilogue(const FgArgs& p, const uint64_t (&ac
                 st[i * 128 + col] = a;
                 st[(i + 1) * 128 + col] = b;
             }
-            fg_barrier(bar);
+            wg_barrier(bar);
             constexpr int RPW = GATED ? 2 : 1;  // rows a warp finishes at once
             const int row0 = RPW * w + (GATED ? lane >> 4 : 0);
             int64_t o = (int64_t)(m0 + c + row0) * p.N + n;
@@ -251,7 +222,7 @@ __device__ __forceinline__ void fg_epilogue(const FgArgs& p, const uint64_t (&ac
                 }
                 sr += 8 * RPW * 128;
             }
-            fg_barrier(bar);
+            wg_barrier(bar);
         }
     }
 }
@@ -573,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     if (SUBS == 2) ph ^= 1;
                 }
             }
-            if (fg_barrier_any(1 + f, !ok)) continue;  // all four warps agree before the staging barriers
+            if (wg_barrier_any(1 + f, !ok)) continue;  // all four warps agree before the staging barriers
             const int m0 = w.m0 + f * ncol;
             if (p.P) {
                 float* P = p.P + ((int64_t)w.slice * (GATED ? 2 : 1) + (GATED && upper ? 1 : 0)) * p.M * p.N;
@@ -645,9 +616,6 @@ __global__ void __launch_bounds__(256) ffn_reduce_kernel(const float* P, int sli
         if (Z) *reinterpret_cast<uint2*>(Z + e) = make_uint2(pack_half2(z[0], z[1]), pack_half2(z[2], z[3]));
     }
 }
-
-const __half* hp(const uint16_t* p) { return reinterpret_cast<const __half*>(p); }
-__half* hp(uint16_t* p) { return reinterpret_cast<__half*>(p); }
 
 struct FgPlan {
     int tn, ks, stages, m_tiles, n_tiles, units;
@@ -795,11 +763,11 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
     a.N = (int)N;
     a.G = (int)G;
     a.tn = pl.tn;
-    a.m_tiles = pl.m_tiles;
-    a.n_tiles = pl.n_tiles;
+    a.raster.m_tiles = pl.m_tiles;
+    a.raster.n_tiles = pl.n_tiles;
+    a.raster.ks = pl.ks;
     // m-tiles whose X stays in L2 (about 48 MB) run down the weights together
-    a.gm = (int)std::max<int64_t>(1, std::min<int64_t>(pl.m_tiles, (48ll << 20) / ((int64_t)pl.tn * K * 2)));
-    a.ks = pl.ks;
+    a.raster.gm = (int)std::max<int64_t>(1, std::min<int64_t>(pl.m_tiles, (48ll << 20) / ((int64_t)pl.tn * K * 2)));
     a.units = pl.units;
     a.stages = pl.stages;
     a.vec = vec_ok(w) && (!gated || vec_ok(*w2)) ? 1 : 0;

@@ -235,10 +235,11 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
 // The epilogue of the sum of `slices` partial products P [slice][layer][M][N], in slice order.
 cudaError_t launch_ffn_reduce(const float* P, int slices, int64_t M, int64_t N, bool gated, const W4Epilogue& ep,
                               cudaStream_t stream);
-// ffn_simple.cu
-// dX = dY W (+ dY2 w2), or with `gate` dG and dU from dH = dY W.
-cudaError_t launch_dx_simple(const uint16_t* dY, const W4Layer& w, const uint16_t* dY2, const W4Layer* w2, int64_t M,
-                             int64_t N, int64_t K, const W4GateGrad* gate, uint16_t* dX, cudaStream_t stream);
+// ffn_dx.cu: dX = dY W (+ dY2 W2), or with `gate` dG and dU from dH = dY W.  ws: ffn_dx_workspace bytes.
+size_t ffn_dx_workspace(int64_t M, int64_t N, int64_t K, int n_layers);
+cudaError_t launch_ffn_dx(const uint16_t* dY, const W4Layer& w, const uint16_t* dY2, const W4Layer* w2, int64_t M,
+                          int64_t N, int64_t K, const W4GateGrad* gate, uint16_t* dX, void* ws, int* status,
+                          cudaStream_t stream);
 // act_backward.cu
 size_t act_backward_workspace(int64_t M, int64_t N);  // bytes, for dbias
 cudaError_t launch_act_backward(const uint16_t* dY, const uint16_t* Z, const uint16_t* U, int64_t M, int64_t N,

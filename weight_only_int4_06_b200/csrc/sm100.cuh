@@ -221,6 +221,19 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
     return d;
 }
 
+// Shared-memory matrix descriptor for an MN-major tile in the 128-byte swizzle layout: along the
+// tile's M (or N) blocks of 64 elements (128-byte rows, one per k; 8 k are an atom of 1024 bytes),
+// `block` bytes from one block of 64 to the next.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t block) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((block >> 4) & 0x3FFFu) << 16;        // leading byte offset: next 64 of M (or N)
+    d |= (uint64_t)(1024u >> 4) << 32;                    // stride byte offset: next 8 of k
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16: fp16 A and B (K-major), fp32 D, M x N.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
     return (1u << 4)                       // D format fp32
@@ -228,6 +241,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
            | ((uint32_t)(N >> 3) << 17)    // N / 8
            | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
+constexpr uint32_t kIdescAMnMajor = 1u << 15;  // A is MN-major
 
 // One lane of a converged warp.  A loop that the whole warp runs, with the tcgen05 and TMA
 // instructions behind this predicate, keeps their operands in uniform registers; behind
