@@ -572,11 +572,32 @@ static cudaError_t zero_half(uint16_t* p, int64_t rows, int64_t cols, cudaStream
     return rows == 0 || cols == 0 ? cudaSuccess : cudaMemsetAsync(p, 0, (size_t)rows * (size_t)cols * 2, s);
 }
 
+// The GEMV up to 16 activation rows where it serves the shape and can bulk-copy the metadata, else the
+// tensor-core product.
+static bool ffn_decode(int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2) {
+    auto meta_ok = [](const W4Layer& l) { return aligned16(l.scales) && aligned16(l.zeros); };
+    return meta_ok(w) && (!w2 || meta_ok(*w2)) && decode_ffn_rows(M, N, K, w2 != nullptr) > 0;
+}
+
+static cudaError_t launch_ffn(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
+                              const W4Epilogue& ep, void* ws, int flags, int* status, cudaStream_t s) {
+    const bool weights_static = (flags & W4_FLAG_WEIGHTS_STATIC) != 0;
+    return ffn_decode(M, N, K, w, w2) ? launch_decode_ffn(X, M, N, K, w, w2, ep, ws, weights_static, status, s)
+                                      : launch_ffn_gemm(X, M, N, K, w, w2, ep, ws, weights_static, status, s);
+}
+
+// Whichever way the metadata's alignment sends the call.
+static size_t ffn_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
+    if (M == 0 || N == 0 || K == 0) return 0;
+    const size_t a = ffn_gemm_workspace(M, N, K, gated), b = decode_ffn_workspace(M, N, K, gated);
+    return a > b ? a : b;
+}
+
 w4_status w4_gemm_fused_workspace_size(int64_t M, int64_t N, int64_t K, int group, size_t* bytes) {
     if (!bytes) return W4_ERR_NULL;
     const w4_status st = ffn_shape(M, N, K, group);
     if (st != W4_OK) return st;
-    *bytes = M > 0 && N > 0 && K > 0 ? ffn_gemm_workspace(M, N, K, false) : 0;
+    *bytes = ffn_workspace(M, N, K, false);
     return W4_OK;
 }
 
@@ -600,8 +621,7 @@ w4_status w4_gemm_fused(const uint16_t* X, int64_t M, int64_t N, int64_t K, cons
     const W4Epilogue ep = {bias, residual, activation, Y, Z, nullptr};
     cudaStream_t s = (cudaStream_t)stream;
     const cudaError_t e = K == 0 ? launch_ffn_reduce(nullptr, 0, M, N, false, ep, s)  // the epilogue of an empty sum
-                                 : launch_ffn_gemm(X, M, N, K, w, nullptr, ep, ws, (flags & W4_FLAG_WEIGHTS_STATIC) != 0,
-                                                   status, s);
+                                 : launch_ffn(X, M, N, K, w, nullptr, ep, ws, flags, status, s);
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
@@ -609,7 +629,7 @@ w4_status w4_gemm_gated_workspace_size(int64_t M, int64_t N, int64_t K, int grou
     if (!bytes) return W4_ERR_NULL;
     const w4_status st = ffn_shape(M, N, K, group);
     if (st != W4_OK) return st;
-    *bytes = M > 0 && N > 0 && K > 0 ? ffn_gemm_workspace(M, N, K, true) : 0;
+    *bytes = ffn_workspace(M, N, K, true);
     return W4_OK;
 }
 
@@ -638,8 +658,7 @@ w4_status w4_gemm_gated(const uint16_t* X, int64_t M, int64_t N, int64_t K, cons
         return W4_OK;
     }
     const W4Epilogue ep = {nullptr, nullptr, activation, H, G, U};
-    const cudaError_t e =
-        launch_ffn_gemm(X, M, N, K, wg, &wu, ep, ws, (flags & W4_FLAG_WEIGHTS_STATIC) != 0, status, s);
+    const cudaError_t e = launch_ffn(X, M, N, K, wg, &wu, ep, ws, flags, status, s);
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 

@@ -40,12 +40,17 @@
 //  * At the end of a tile every consumer warp parks its partial sums in a shared slot and moves
 //    on; a reducer warp adds the warps' partials in warp order (deterministic) and writes Y, so
 //    the ring never waits for a reduction.
+//  * EPI 1 and 2 (w4_gemm_fused, w4_gemm_gated) give the reducer an epilogue: bias, activation and
+//    residual, or the gate.  A gated tile is 8 gate rows and the 8 up rows of the same outputs (two
+//    boxes per stage), so both factors of an output meet in one slot; everything before the reducer
+//    is the plain kernel's.
 //  * The kernel is instantiated per activation-row bound MT (1, 2, 4, 8): columns >= MT of the
 //    MMA fragments are never folded or parked.  MT = 16 (split mode, 16-group stages) feeds every
 //    dequantised A fragment to two MMAs, for activation rows 0-7 and 8-15.
 #include <algorithm>
 #include <mutex>
 
+#include "activation.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -217,13 +222,44 @@ __device__ __forceinline__ void ds_group16(uint32_t a_addr, uint32_t b_addr, uin
     acc[7] = fmaf(fsb, c1[3] - fmaf(fzb, __uint_as_float(v.w), __uint_as_float(v.z)), acc[7]);
 }
 
-template <int MT, int SG, bool KS>
+// What an instantiation's epilogue adds to the kernel's arguments.
+template <int EPI>
+struct DsExtra {};
+template <>
+struct DsExtra<1> {
+    const __half* bias;
+    const __half* residual;
+    __half* Z;
+    int act;
+};
+template <>
+struct DsExtra<2> {
+    CUtensorMap tmW2, tmS2, tmZ2;  // the up projection's (tmS2, tmZ2: split mode)
+    const unsigned short* scales2;
+    const uint8_t* zeros2;
+    __half* G;
+    __half* U;
+    int act;
+};
+
+// Epilogue of one output element e (column n).
+template <int ACT>
+__device__ __forceinline__ float ds_finish(const DsExtra<1>& ex, float z, int64_t e, int n) {
+    if (ex.bias) z += __half2float(ex.bias[n]);
+    if (ex.Z) ex.Z[e] = __float2half_rn(z);
+    float y = act_fwd<ACT>(z);
+    if (ex.residual) y += __half2float(ex.residual[e]);
+    return y;
+}
+
+template <int MT, int SG, bool KS, int EPI>
 __global__ void __launch_bounds__(DS_THREADS, 1)
     decode_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
                          const __grid_constant__ CUtensorMap tmZ, const __half* __restrict__ X,
                          const unsigned short* __restrict__ scales, const uint8_t* __restrict__ zeros,
-                         __half* __restrict__ Y, float* __restrict__ P, int M, int N, int K, int n_tiles, int ns,
-                         int nms, int ncs, int weights_early, int* status) {
+                         __half* Y, float* __restrict__ P, int M, int N, int K, int n_tiles, int ns, int nms, int ncs,
+                         int weights_early, int* status, const __grid_constant__ DsExtra<EPI> ex) {
+    constexpr int TR = EPI == 2 ? 8 : 16;            // rows of each layer in a tile
     constexpr int ROWB = SG * 64;                    // bytes of one row in a stage
     constexpr uint32_t STAGE_BYTES = 16u * ROWB;
     constexpr int GPW = SG / DS_CW;                  // groups per consumer warp per stage
@@ -278,6 +314,7 @@ __global__ void __launch_bounds__(DS_THREADS, 1)
                 prefetch_tmap(&tmS);
                 prefetch_tmap(&tmZ);
             }
+            if constexpr (EPI == 2) prefetch_tmap(&ex.tmW2);
             if (!weights_early) pdl_wait();
             int issued = 0, t = t0, kc = 0, s = 0, ms = 0;
             uint32_t ph = 0, mph = 0;
@@ -297,14 +334,25 @@ __global__ void __launch_bounds__(DS_THREADS, 1)
                     const int kg = kc0 + kc;
                     const uint32_t mdst = sbase + L.meta + (uint32_t)s * L.mslot;
                     mbar_arrive_expect_tx(full_bar(s), STAGE_BYTES + ds_stage_meta_bytes(SG));
-                    tma_load_2d(sbase + L.ring + s * STAGE_BYTES, &tmW, kg * (ROWB / 8), t * 16, full_bar(s));
-                    tma_load_2d(mdst, &tmS, kg * SG, t * 16, full_bar(s));
-                    tma_load_2d(mdst + 32u * SG, &tmZ, kg * SG, t * 16, full_bar(s));
+                    tma_load_2d(sbase + L.ring + s * STAGE_BYTES, &tmW, kg * (ROWB / 8), t * TR, full_bar(s));
+                    tma_load_2d(mdst, &tmS, kg * SG, t * TR, full_bar(s));
+                    tma_load_2d(mdst + 32u * SG, &tmZ, kg * SG, t * TR, full_bar(s));
+                    if constexpr (EPI == 2) {
+                        tma_load_2d(sbase + L.ring + s * STAGE_BYTES + STAGE_BYTES / 2, &ex.tmW2, kg * (ROWB / 8), t * TR,
+                                    full_bar(s));
+                        tma_load_2d(mdst + 16u * SG, &ex.tmS2, kg * SG, t * TR, full_bar(s));
+                        tma_load_2d(mdst + 40u * SG, &ex.tmZ2, kg * SG, t * TR, full_bar(s));
+                    }
                 } else {
                     uint32_t sb = 0, zb = 0;
-                    const int64_t mofs = (int64_t)t * 16 * G;  // first metadata entry of the tile
+                    const int64_t mofs = (int64_t)t * TR * G;  // first metadata entry of the tile
                     const uint32_t mdst = L.meta + ms * L.mslot;
-                    if (kc == 0) {  // the tile's metadata rides on its first stage
+                    if constexpr (EPI == 2) {  // G is even: both layers' 8 G zero points are whole 16 bytes
+                        if (kc == 0) {
+                            sb = (uint32_t)(32 * G);
+                            zb = (uint32_t)(16 * G);
+                        }
+                    } else if (kc == 0) {  // the tile's metadata rides on its first stage
                         const int rows = N - t * 16 < 16 ? N - t * 16 : 16;  // 8 or 16 (N % 8 == 0)
                         sb = (uint32_t)(rows * 2 * G);
                         zb = (uint32_t)(rows * G) & ~15u;
@@ -313,9 +361,20 @@ __global__ void __launch_bounds__(DS_THREADS, 1)
                                 *reinterpret_cast<const uint2*>(zeros + mofs + zb);
                     }
                     mbar_arrive_expect_tx(full_bar(s), STAGE_BYTES + sb + zb);
-                    tma_load_2d(sbase + L.ring + s * STAGE_BYTES, &tmW, kc * (ROWB / 8), t * 16, full_bar(s));
-                    if (sb) bulk_load_1d(sbase + mdst, scales + mofs, sb, full_bar(s));
-                    if (zb) bulk_load_1d(sbase + mdst + 32 * G, zeros + mofs, zb, full_bar(s));
+                    tma_load_2d(sbase + L.ring + s * STAGE_BYTES, &tmW, kc * (ROWB / 8), t * TR, full_bar(s));
+                    if constexpr (EPI == 2) {
+                        tma_load_2d(sbase + L.ring + s * STAGE_BYTES + STAGE_BYTES / 2, &ex.tmW2, kc * (ROWB / 8), t * TR,
+                                    full_bar(s));
+                        if (sb) {
+                            bulk_load_1d(sbase + mdst, scales + mofs, sb / 2, full_bar(s));
+                            bulk_load_1d(sbase + mdst + 16 * G, ex.scales2 + mofs, sb / 2, full_bar(s));
+                            bulk_load_1d(sbase + mdst + 32 * G, zeros + mofs, zb / 2, full_bar(s));
+                            bulk_load_1d(sbase + mdst + 40 * G, ex.zeros2 + mofs, zb / 2, full_bar(s));
+                        }
+                    } else {
+                        if (sb) bulk_load_1d(sbase + mdst, scales + mofs, sb, full_bar(s));
+                        if (zb) bulk_load_1d(sbase + mdst + 32 * G, zeros + mofs, zb, full_bar(s));
+                    }
                 }
                 ++issued;
                 if (++kc == NCl) {
@@ -336,7 +395,7 @@ __global__ void __launch_bounds__(DS_THREADS, 1)
         pdl_wait();  // Y may be read by the preceding kernel
         int rs = 0;
         uint32_t rph = 0;
-        float* Pl = KS && P ? P + (int64_t)blockIdx.y * M * N : nullptr;  // this slice's partials
+        float* Pl = KS && P ? P + (int64_t)blockIdx.y * (EPI == 2 ? 2 : 1) * M * N : nullptr;  // this slice's partials
         for (int t = t0; t < t1; ++t) {
             if (!mbar_wait_bounded(tile_full(rs), rph, abort_flag)) {
                 *abort_flag = 1;
@@ -347,15 +406,43 @@ __global__ void __launch_bounds__(DS_THREADS, 1)
 #pragma unroll
             for (int o0 = 0; o0 < 16 * MT; o0 += 32) {
                 const int o = o0 + lane, row = o / MT, m = o - row * MT;
-                const int n = t * 16 + row;
-                if (o < 16 * MT && m < M && n < N) {
+                const int n = t * TR + (EPI == 2 ? row & 7 : row);
+                if (EPI == 2 && !(KS && P)) {
+                    // rows 0-7: the gate; 8 MT slots further, the same output's up projection
+                    if (o < 8 * MT && m < M && n < N) {
+                        float g = 0.0f, u = 0.0f;
+#pragma unroll
+                        for (int w = 0; w < DS_CW; ++w) {
+                            g += rsl[w * (16 * MT) + o];
+                            u += rsl[w * (16 * MT) + o + 8 * MT];
+                        }
+                        if constexpr (EPI == 2) {
+                            const int64_t e = (int64_t)m * N + n;
+                            if (ex.G) {
+                                ex.G[e] = __float2half_rn(g);
+                                ex.U[e] = __float2half_rn(u);
+                            }
+                            dispatch_act(ex.act, [&](auto act) {
+                                Y[e] = __float2half_rn(act_fwd<decltype(act)::value>(g) * u);
+                                return cudaSuccess;
+                            });
+                        }
+                    }
+                } else if (o < 16 * MT && m < M && n < N) {
                     float sum = 0.0f;
 #pragma unroll
                     for (int w = 0; w < DS_CW; ++w) sum += rsl[w * (16 * MT) + o];
-                    if (KS && P)
-                        Pl[(int64_t)m * N + n] = sum;
-                    else
-                        Y[(int64_t)m * N + n] = __float2half_rn(sum);
+                    const int64_t e = (int64_t)m * N + n;
+                    if (KS && P) {
+                        Pl[(EPI == 2 && row >= 8 ? (int64_t)M * N : 0) + e] = sum;
+                    } else if constexpr (EPI == 1) {
+                        dispatch_act(ex.act, [&](auto act) {
+                            Y[e] = __float2half_rn(ds_finish<decltype(act)::value>(ex, sum, e, n));
+                            return cudaSuccess;
+                        });
+                    } else {
+                        Y[e] = __float2half_rn(sum);
+                    }
                 }
             }
             __syncwarp();
@@ -646,10 +733,11 @@ size_t decode_stream_workspace(int64_t M, int64_t N, int64_t K) {
     return need;
 }
 
-template <int MT, int SG, bool KS>
+template <int MT, int SG, bool KS, int EPI>
 static cudaError_t ds_launch(const CUtensorMap& tm, const CUtensorMap& tmS, const CUtensorMap& tmZ, const uint16_t* X,
                              int64_t M, int64_t N, int64_t K, const uint16_t* scales, const uint8_t* zeros, uint16_t* Y,
-                             float* P, const DecodePlan& p, bool weights_static, int* status, cudaStream_t stream) {
+                             float* P, const DecodePlan& p, bool weights_static, int* status, cudaStream_t stream,
+                             const DsExtra<EPI>& ex) {
     static std::once_flag once[64];
     static cudaError_t attr_err[64];
     int dev = 0;
@@ -657,7 +745,7 @@ static cudaError_t ds_launch(const CUtensorMap& tm, const CUtensorMap& tmS, cons
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::call_once(once[dev], [&]() {
-        attr_err[dev] = cudaFuncSetAttribute(decode_stream_kernel<MT, SG, KS>,
+        attr_err[dev] = cudaFuncSetAttribute(decode_stream_kernel<MT, SG, KS, EPI>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DS_FULL_SMEM);
     });
     if (attr_err[dev] != cudaSuccess) return attr_err[dev];
@@ -671,28 +759,65 @@ static cudaError_t ds_launch(const CUtensorMap& tm, const CUtensorMap& tmS, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = weights_static ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_stream_kernel<MT, SG, KS>, tm, tmS, tmZ,
+    return cudaLaunchKernelEx(&cfg, decode_stream_kernel<MT, SG, KS, EPI>, tm, tmS, tmZ,
                               reinterpret_cast<const __half*>(X), reinterpret_cast<const unsigned short*>(scales),
                               zeros, reinterpret_cast<__half*>(Y), P, (int)M, (int)N, (int)K, p.n_tiles, p.ns, p.nms,
-                              p.ncs, weights_static ? 1 : 0, status);
+                              p.ncs, weights_static ? 1 : 0, status, ex);
 }
 
-template <bool KS>
+template <bool KS, int EPI>
 static cudaError_t ds_launch_mt(const CUtensorMap& tm, const CUtensorMap& tmS, const CUtensorMap& tmZ,
                                 const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint16_t* scales,
                                 const uint8_t* zeros, uint16_t* Y, float* P, const DecodePlan& p, bool ws_,
-                                int* status, cudaStream_t stream) {
+                                int* status, cudaStream_t stream, const DsExtra<EPI>& ex) {
+    auto launch = [&](auto mt, auto sg) {
+        return ds_launch<decltype(mt)::value, decltype(sg)::value, KS, EPI>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, P, p,
+                                                                           ws_, status, stream, ex);
+    };
+    using I32 = std::integral_constant<int, 32>;
     switch (p.mt) {
-        case 1: return ds_launch<1, 32, KS>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, P, p, ws_, status, stream);
-        case 2: return ds_launch<2, 32, KS>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, P, p, ws_, status, stream);
-        case 4: return ds_launch<4, 32, KS>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, P, p, ws_, status, stream);
-        case 8: return ds_launch<8, 32, KS>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, P, p, ws_, status, stream);
+        case 1: return launch(std::integral_constant<int, 1>{}, I32{});
+        case 2: return launch(std::integral_constant<int, 2>{}, I32{});
+        case 4: return launch(std::integral_constant<int, 4>{}, I32{});
+        case 8: return launch(std::integral_constant<int, 8>{}, I32{});
         default:
             if constexpr (KS)
-                return ds_launch<16, 16, true>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, P, p, ws_, status, stream);
+                return launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
             else
                 return cudaErrorInvalidValue;  // the 16-row instantiation runs in split mode only
     }
+}
+
+// Tensor maps of one layer for `rows`-row tiles: packed rows as 8-byte elements (a box of 8 SG elements
+// is one stage's share of a row) and, in split mode, [rows][SG] boxes of the scales and zero points.
+static bool ds_maps(const DecodePlan& p, const uint32_t* packed, const uint16_t* scales, const uint8_t* zeros, int64_t N,
+                    int64_t K, uint32_t rows, CUtensorMap* tm, CUtensorMap* tmS, CUtensorMap* tmZ) {
+    if (!make_tensor_map_2d(tm, packed, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, (uint64_t)(K / 16), (uint64_t)N,
+                            (uint32_t)(8 * p.sg), rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return false;
+    if (p.ncs == 0) {
+        *tmS = *tm;
+        *tmZ = *tm;
+        return true;
+    }
+    const uint64_t G = (uint64_t)(K / 128);
+    return make_tensor_map_2d(tmS, scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, G, (uint64_t)N, (uint32_t)p.sg, rows,
+                              CU_TENSOR_MAP_SWIZZLE_NONE) &&
+           make_tensor_map_2d(tmZ, zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, G, (uint64_t)N, (uint32_t)p.sg, rows,
+                              CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// One launch (of M <= 16 rows) with its K slices' partials in P (null: one slice).
+template <int EPI>
+static cudaError_t ds_run(const DecodePlan& p, const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
+                          const uint16_t* scales, const uint8_t* zeros, uint16_t* Y, float* P, bool weights_static,
+                          int* status, cudaStream_t stream, const DsExtra<EPI>& ex) {
+    CUtensorMap tm, tmS, tmZ;
+    if (!ds_maps(p, packed, scales, zeros, N, K, EPI == 2 ? 8 : 16, &tm, &tmS, &tmZ)) return cudaErrorInvalidValue;
+    if (p.ncs == 0)
+        return ds_launch_mt<false, EPI>(tm, tm, tm, X, M, N, K, scales, zeros, Y, nullptr, p, weights_static, status, stream,
+                                        ex);
+    return ds_launch_mt<true, EPI>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, P, p, weights_static, status, stream, ex);
 }
 
 cudaError_t launch_decode_stream(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
@@ -700,29 +825,80 @@ cudaError_t launch_decode_stream(const uint16_t* X, int64_t M, int64_t N, int64_
                                  bool weights_static, int* status, cudaStream_t stream) {
     DecodePlan p;
     if (!plan_decode_stream(M, N, K, &p)) return cudaErrorInvalidValue;
-    CUtensorMap tm;  // packed rows as 8-byte elements: a box of 8 SG elements is one stage's share of a row
-    if (!make_tensor_map_2d(&tm, packed, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, (uint64_t)(K / 16), (uint64_t)N,
-                            (uint32_t)(8 * p.sg), 16, CU_TENSOR_MAP_SWIZZLE_NONE))
-        return cudaErrorInvalidValue;
-    if (p.ncs == 0) return ds_launch_mt<false>(tm, tm, tm, X, M, N, K, scales, zeros, Y, nullptr, p, weights_static,
-                                               status, stream);
-    // split mode: [16][SG] boxes of the scales and zero points; with several slices fp32 partials
-    // in ws, then their sum
-    CUtensorMap tmS, tmZ;
-    const uint64_t G = (uint64_t)(K / 128);
-    if (!make_tensor_map_2d(&tmS, scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, G, (uint64_t)N, (uint32_t)p.sg, 16,
-                            CU_TENSOR_MAP_SWIZZLE_NONE) ||
-        !make_tensor_map_2d(&tmZ, zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, G, (uint64_t)N, (uint32_t)p.sg, 16,
-                            CU_TENSOR_MAP_SWIZZLE_NONE))
-        return cudaErrorInvalidValue;
-    if (p.ks == 1)
-        return ds_launch_mt<true>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, nullptr, p, weights_static, status,
-                                  stream);
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15)) return cudaErrorInvalidValue;
-    float* P = static_cast<float*>(ws);
-    cudaError_t e = ds_launch_mt<true>(tm, tmS, tmZ, X, M, N, K, scales, zeros, Y, P, p, weights_static, status, stream);
-    if (e != cudaSuccess) return e;
+    // with several slices fp32 partials in ws, then their sum
+    const bool split = p.ncs > 0 && p.ks > 1;
+    if (split && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15))) return cudaErrorInvalidValue;
+    float* P = split ? static_cast<float*>(ws) : nullptr;
+    const cudaError_t e = ds_run<0>(p, X, M, N, K, packed, scales, zeros, Y, P, weights_static, status, stream, {});
+    if (e != cudaSuccess || !split) return e;
     return launch_splitk_reduce(P, p.ks, M * N, Y, stream);
+}
+
+// ---------------------------------------------------------------- with an epilogue (w4_gemm_fused, w4_gemm_gated)
+// Activation rows per launch: the plain GEMV's where they fit, else fewer (long K whose groups cannot
+// be sliced); 0: the shape is not served.
+int64_t decode_ffn_rows(int64_t M, int64_t N, int64_t K, bool gated) {
+    if (M > DS_MAXM || (gated && K % 256 != 0)) return 0;
+    DecodePlan p;
+    for (int64_t rows : std::initializer_list<int64_t>{decode_stream_rows(M, K), 4, 2, 1})
+        if (plan_decode_stream(std::min(M, rows), gated ? 2 * N : N, K, &p)) return rows;
+    return 0;
+}
+
+int64_t decode_ffn_launches(int64_t M, int64_t N, int64_t K, bool gated) {
+    const int64_t rows = decode_ffn_rows(M, N, K, gated);
+    return rows ? (M + rows - 1) / rows : 0;
+}
+
+size_t decode_ffn_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
+    const int64_t rows = decode_ffn_rows(M, N, K, gated);
+    size_t need = 0;
+    if (rows == 0) return 0;
+    for (int64_t mc : std::initializer_list<int64_t>{std::min(M, rows), M % rows}) {
+        if (mc < 1) continue;
+        const int ks = decode_stream_slices(mc, K);
+        if (ks > 1) need = std::max(need, (size_t)ks * (size_t)mc * (size_t)N * (gated ? 8 : 4));
+    }
+    return need;
+}
+
+cudaError_t launch_decode_ffn(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
+                              const W4Epilogue& ep, void* ws, bool weights_static, int* status, cudaStream_t stream) {
+    const int64_t rows = decode_ffn_rows(M, N, K, w2 != nullptr);
+    if (rows == 0) return cudaErrorInvalidValue;
+    auto at = [](const uint16_t* q, int64_t o) { return q ? const_cast<uint16_t*>(q) + o : nullptr; };
+    auto hf = [](const uint16_t* q) { return reinterpret_cast<__half*>(const_cast<uint16_t*>(q)); };
+    for (int64_t m0 = 0; m0 < M; m0 += rows) {
+        const int64_t mc = std::min(rows, M - m0), o = m0 * N;
+        DecodePlan p;
+        if (!plan_decode_stream(mc, w2 ? 2 * N : N, K, &p)) return cudaErrorInvalidValue;
+        const bool split = p.ncs > 0 && p.ks > 1;
+        if (split && !ws) return cudaErrorInvalidValue;
+        float* P = split ? static_cast<float*>(ws) : nullptr;
+        W4Epilogue e1 = ep;
+        e1.residual = at(ep.residual, o);
+        e1.Y = at(ep.Y, o);
+        e1.Z = at(ep.Z, o);
+        e1.U = at(ep.U, o);
+        cudaError_t e;
+        if (w2) {
+            DsExtra<2> ex = {};
+            if (!ds_maps(p, w2->packed, w2->scales, w2->zeros, N, K, 8, &ex.tmW2, &ex.tmS2, &ex.tmZ2))
+                return cudaErrorInvalidValue;
+            ex.scales2 = w2->scales;
+            ex.zeros2 = w2->zeros;
+            ex.G = hf(e1.Z);
+            ex.U = hf(e1.U);
+            ex.act = ep.activation;
+            e = ds_run<2>(p, X + m0 * K, mc, N, K, w.packed, w.scales, w.zeros, e1.Y, P, weights_static, status, stream, ex);
+        } else {
+            const DsExtra<1> ex = {hf(ep.bias), hf(e1.residual), hf(e1.Z), ep.activation};
+            e = ds_run<1>(p, X + m0 * K, mc, N, K, w.packed, w.scales, w.zeros, e1.Y, P, weights_static, status, stream, ex);
+        }
+        if (e != cudaSuccess) return e;
+        if (split && (e = launch_ffn_reduce(P, p.ks, mc, N, w2 != nullptr, e1, stream)) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace w4
