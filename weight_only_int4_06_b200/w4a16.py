@@ -6,7 +6,6 @@ no fallback: if libw4a16.so is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -619,6 +618,8 @@ def awq_clip_search(X: torch.Tensor, W: torch.Tensor, act_scale: torch.Tensor | 
 # ------------------------------------------------------------------ feed-forward operators
 def _arg(t: torch.Tensor, dtype, shape, dev, name) -> int:
     """Device address of a tensor argument, its type, shape, device and layout checked."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -627,9 +628,7 @@ def _arg(t: torch.Tensor, dtype, shape, dev, name) -> int:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -638,64 +637,62 @@ def _matrix(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _layer_args(layer, N: int, K: int, group: int, dev, name: str):
-    packed, scales, zeros = layer
-    G = K // group if group > 0 else 0
+def _layer_args(packed, scales, zeros, N: int, K: int, group: int, dev, name: str):
+    meta = (N, K // group if group > 0 else 0)
     return (_arg(packed, torch.int32, (N, K // 8), dev, name + "packed"),
-            _arg(scales, torch.float16, (N, G), dev, name + "scales"),
-            _arg(zeros, torch.uint8, (N, G), dev, name + "zeros"))
+            _arg(scales, torch.float16, meta, dev, name + "scales"),
+            _arg(zeros, torch.uint8, meta, dev, name + "zeros"))
 
 
-def _raw_stream(dev, stream) -> int:
-    """The cudaStream_t of `stream`, or of the device's current stream."""
+def _other_context(dev, stream):
+    """None where a call runs on the tensors' device and that device's current stream and both are
+    current already (nothing to switch: the usual case, kept short because a decode step's calls are
+    as short as their launch); else the context to allocate and launch in, so that new outputs and
+    workspaces belong to `stream`."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+    return torch.cuda.stream(stream)
 
 
-def _on(dev, stream):
-    """Context in which a call allocates and launches: the tensors' device, and `stream` when one is
-    given (so that new outputs and workspaces belong to it)."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, expected {dev}")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != dev.index:
-        return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+def _current_stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 _ffn_ws_cache: dict = {}
 
 
-def _ffn_workspace(name: str, dims: tuple, workspace, dev):
+def _ffn_workspace(name: str, dims: tuple, workspace, like: torch.Tensor):
     """(address, bytes) of the caller's workspace or, where it has none or one too small, of a new
     one, and the tensor that holds it."""
     need = _ffn_ws_cache.get((name, dims))
     if need is None:
         n = ctypes.c_size_t(0)
         _check(getattr(lib(), name)(*dims, ctypes.byref(n)), name)
+        if len(_ffn_ws_cache) >= 4096:  # ragged batches: every M is a key
+            _ffn_ws_cache.clear()
         need = _ffn_ws_cache[(name, dims)] = n.value
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        if workspace.device != like.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
         have = workspace.numel() * workspace.element_size()
         if have >= need:
             return workspace.data_ptr(), have, workspace
     if need == 0:
         return None, 0, None
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    workspace = like.new_empty(need, dtype=torch.uint8)
     return workspace.data_ptr(), need, workspace
 
 
-def _out(t, shape, dev, name):
-    """An output tensor (a new one when none is given) and its address."""
+def _out(t, shape, like: torch.Tensor, name):
+    """An output tensor (a new fp16 one when none is given) and its address."""
     if t is None:
-        t = torch.empty(shape, dtype=torch.float16, device=dev)
+        t = like.new_empty(shape)
         return t, t.data_ptr()
-    return t, _arg(t, torch.float16, shape, dev, name)
+    return t, _arg(t, torch.float16, shape, like.device, name)
 
 
 def _on_gpu(t: torch.Tensor, name: str):
@@ -720,16 +717,20 @@ def w4_gemm_fused(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, z
     M, K = _matrix(X, "X")
     N = _matrix(packed, "packed")[0]
     dev = _on_gpu(X, "X")
+    other = _other_context(dev, stream)
+    if other is not None:
+        with other:
+            return w4_gemm_fused(X, packed, scales, zeros, bias, activation, residual, save_pre, group, out, workspace,
+                                 flags)
     xp = _arg(X, torch.float16, (M, K), dev, "X")
-    wp, sp, zp = _layer_args((packed, scales, zeros), N, K, group, dev, "")
+    w = _layer_args(packed, scales, zeros, N, K, group, dev, "")
     bp = _arg(bias, torch.float16, (N,), dev, "bias") if bias is not None else None
     rp = _arg(residual, torch.float16, (M, N), dev, "residual") if residual is not None else None
-    with _on(dev, stream):
-        wsp, wsb, workspace = _ffn_workspace("w4_gemm_fused_workspace_size", (M, N, K, group), workspace, dev)
-        Y, yp = _out(out, (M, N), dev, "out")
-        Z, pre = _out(None, (M, N), dev, "Z") if save_pre else (None, None)
-        _check(lib().w4_gemm_fused(xp, M, N, K, wp, sp, zp, group, bp, activation, rp, yp, pre, wsp, wsb, flags,
-                                   _raw_stream(dev, stream)), "w4_gemm_fused")
+    wsp, wsb, workspace = _ffn_workspace("w4_gemm_fused_workspace_size", (M, N, K, group), workspace, X)
+    Y, yp = _out(out, (M, N), X, "out")
+    Z, pre = _out(None, (M, N), X, "Z") if save_pre else (None, None)
+    _check(lib().w4_gemm_fused(xp, M, N, K, *w, group, bp, activation, rp, yp, pre, wsp, wsb, flags,
+                               _current_stream(dev)), "w4_gemm_fused")
     return (Y, Z) if save_pre else Y
 
 
@@ -747,16 +748,19 @@ def w4_gemm_gated(X: torch.Tensor, gate, up, activation: int = ACT_SILU, save_pr
     M, K = _matrix(X, "X")
     N = _matrix(gate[0], "gate packed")[0]
     dev = _on_gpu(X, "X")
+    other = _other_context(dev, stream)
+    if other is not None:
+        with other:
+            return w4_gemm_gated(X, gate, up, activation, save_pre, group, out, workspace, flags)
     xp = _arg(X, torch.float16, (M, K), dev, "X")
-    g = _layer_args(gate, N, K, group, dev, "gate ")
-    u = _layer_args(up, N, K, group, dev, "up ")
-    with _on(dev, stream):
-        wsp, wsb, workspace = _ffn_workspace("w4_gemm_gated_workspace_size", (M, N, K, group), workspace, dev)
-        H, hp = _out(out, (M, N), dev, "out")
-        G, gp = _out(None, (M, N), dev, "G") if save_pre else (None, None)
-        U, up_ = _out(None, (M, N), dev, "U") if save_pre else (None, None)
-        _check(lib().w4_gemm_gated(xp, M, N, K, *g, *u, group, activation, hp, gp, up_, wsp, wsb, flags,
-                                   _raw_stream(dev, stream)), "w4_gemm_gated")
+    g = _layer_args(*gate, N, K, group, dev, "gate ")
+    u = _layer_args(*up, N, K, group, dev, "up ")
+    wsp, wsb, workspace = _ffn_workspace("w4_gemm_gated_workspace_size", (M, N, K, group), workspace, X)
+    H, hp = _out(out, (M, N), X, "out")
+    G, gp = _out(None, (M, N), X, "G") if save_pre else (None, None)
+    U, up_ = _out(None, (M, N), X, "U") if save_pre else (None, None)
+    _check(lib().w4_gemm_gated(xp, M, N, K, *g, *u, group, activation, hp, gp, up_, wsp, wsb, flags,
+                               _current_stream(dev)), "w4_gemm_gated")
     return (H, G, U) if save_pre else H
 
 
@@ -773,20 +777,22 @@ def w4_gemm_dx(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
     M, N = _matrix(dY, "dY")
     K = _matrix(packed, "packed")[1] * 8
     dev = _on_gpu(dY, "dY")
+    other = _other_context(dev, stream)
+    if other is not None:
+        with other:
+            return w4_gemm_dx(dY, packed, scales, zeros, dY2, weights2, group, out, workspace)
     yp = _arg(dY, torch.float16, (M, N), dev, "dY")
-    w = _layer_args((packed, scales, zeros), N, K, group, dev, "")
+    w = _layer_args(packed, scales, zeros, N, K, group, dev, "")
     if (dY2 is None) != (weights2 is None):
         raise ValueError("dY2 and weights2 go together")
     yp2, w2 = None, (None, None, None)
     if dY2 is not None:
         yp2 = _arg(dY2, torch.float16, (M, N), dev, "dY2")
-        w2 = _layer_args(weights2, N, K, group, dev, "second ")
-    with _on(dev, stream):
-        wsp, wsb, workspace = _ffn_workspace("w4_gemm_dx_workspace_size", (M, N, K, 1 if dY2 is None else 2, group),
-                                             workspace, dev)
-        dX, xp = _out(out, (M, K), dev, "out")
-        _check(lib().w4_gemm_dx(yp, M, N, K, *w, yp2, *w2, group, xp, wsp, wsb, _raw_stream(dev, stream)),
-               "w4_gemm_dx")
+        w2 = _layer_args(*weights2, N, K, group, dev, "second ")
+    wsp, wsb, workspace = _ffn_workspace("w4_gemm_dx_workspace_size", (M, N, K, 1 if dY2 is None else 2, group),
+                                         workspace, dY)
+    dX, xp = _out(out, (M, K), dY, "out")
+    _check(lib().w4_gemm_dx(yp, M, N, K, *w, yp2, *w2, group, xp, wsp, wsb, _current_stream(dev)), "w4_gemm_dx")
     return dX
 
 
@@ -798,16 +804,19 @@ def w4_gemm_dx_gated(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
     M, N = _matrix(dY, "dY")
     K = _matrix(packed, "packed")[1] * 8
     dev = _on_gpu(dY, "dY")
+    other = _other_context(dev, stream)
+    if other is not None:
+        with other:
+            return w4_gemm_dx_gated(dY, packed, scales, zeros, G, U, activation, group, out, workspace)
     yp = _arg(dY, torch.float16, (M, N), dev, "dY")
-    w = _layer_args((packed, scales, zeros), N, K, group, dev, "")
+    w = _layer_args(packed, scales, zeros, N, K, group, dev, "")
     gp = _arg(G, torch.float16, (M, K), dev, "G")
     up = _arg(U, torch.float16, (M, K), dev, "U")
-    with _on(dev, stream):
-        wsp, wsb, workspace = _ffn_workspace("w4_gemm_dx_workspace_size", (M, N, K, 1, group), workspace, dev)
-        dG, dgp = _out(out[0] if out is not None else None, (M, K), dev, "out[0]")
-        dU, dup = _out(out[1] if out is not None else None, (M, K), dev, "out[1]")
-        _check(lib().w4_gemm_dx_gated(yp, M, N, K, *w, group, gp, up, activation, dgp, dup, wsp, wsb,
-                                      _raw_stream(dev, stream)), "w4_gemm_dx_gated")
+    wsp, wsb, workspace = _ffn_workspace("w4_gemm_dx_workspace_size", (M, N, K, 1, group), workspace, dY)
+    dG, dgp = _out(out[0] if out is not None else None, (M, K), dY, "out[0]")
+    dU, dup = _out(out[1] if out is not None else None, (M, K), dY, "out[1]")
+    _check(lib().w4_gemm_dx_gated(yp, M, N, K, *w, group, gp, up, activation, dgp, dup, wsp, wsb,
+                                  _current_stream(dev)), "w4_gemm_dx_gated")
     return dG, dU
 
 
@@ -825,6 +834,10 @@ def w4_act_backward(dY: torch.Tensor, Z: torch.Tensor | None, U: torch.Tensor | 
     out: dZ, or (dG, dU), possibly the inputs' own buffers.  With ACT_NONE and no U, Z may be None."""
     M, N = _matrix(dY, "dY")
     dev = _on_gpu(dY, "dY")
+    other = _other_context(dev, stream)
+    if other is not None:
+        with other:
+            return w4_act_backward(dY, Z, U, activation, bias_grad, out, workspace)
     yp = _arg(dY, torch.float16, (M, N), dev, "dY")
     zp = _arg(Z, torch.float16, (M, N), dev, "Z") if Z is not None else None
     up = _arg(U, torch.float16, (M, N), dev, "U") if U is not None else None
@@ -832,16 +845,14 @@ def w4_act_backward(dY: torch.Tensor, Z: torch.Tensor | None, U: torch.Tensor | 
         out = (out, None)
     elif out is None:
         out = (None, None)
-    with _on(dev, stream):
-        dZ, dzp = _out(out[0], (M, N), dev, "out")
-        dU, dup = _out(out[1], (M, N), dev, "out[1]") if U is not None else (None, None)
-        dbias = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
-        wsp, wsb = None, 0
-        if bias_grad:
-            wsp, wsb, workspace = _ffn_workspace("w4_act_backward_workspace_size", (M, N), workspace, dev)
-        _check(lib().w4_act_backward(yp, zp, up, M, N, activation, dzp, dup,
-                                     dbias.data_ptr() if bias_grad else None, wsp, wsb, _raw_stream(dev, stream)),
-               "w4_act_backward")
+    dZ, dzp = _out(out[0], (M, N), dY, "out")
+    dU, dup = _out(out[1], (M, N), dY, "out[1]") if U is not None else (None, None)
+    dbias = dY.new_empty(N, dtype=torch.float32) if bias_grad else None
+    wsp, wsb = None, 0
+    if bias_grad:
+        wsp, wsb, workspace = _ffn_workspace("w4_act_backward_workspace_size", (M, N), workspace, dY)
+    _check(lib().w4_act_backward(yp, zp, up, M, N, activation, dzp, dup, dbias.data_ptr() if bias_grad else None, wsp,
+                                 wsb, _current_stream(dev)), "w4_act_backward")
     if U is not None:
         return dZ, dU
     return (dZ, dbias) if bias_grad else dZ
