@@ -3,10 +3,15 @@
 //   dZ = dY * act'(Z), dbias[n] = sum_m dZ[m, n]          (U null)
 //   dG = dH * U * act'(G), dU = dH * act(G)               (gated: Z holds G, dY holds dH)
 //
-// Bound by HBM: 6 bytes per element (10 gated) against about ten fp32 operations.  A thread takes 8
-// neighbouring columns (16-byte loads and stores).  For dbias a CTA walks down a block of rows with
-// its columns' sums in registers (fp32, row order), the row blocks' partials go to the workspace and
-// a second launch adds them in block order: deterministic, no atomics.  dZ enters the sum unrounded.
+// Bound by HBM: 6 bytes per element (10 gated) against ten to thirty fp32 operations.  A thread takes 8
+// neighbouring columns (16-byte loads and stores) of every rl-th row of its CTA's block of rows, four rows'
+// loads in flight together (outputs may be the inputs' own buffers, so nothing moves a load over a store).
+// A CTA is cw column vectors by rl = 256 / cw row lanes, so narrow matrices fill it too.  For dbias the
+// thread keeps its columns' sums in registers (fp32, row order), the CTA's row lanes are added in order in
+// shared memory, the row blocks' sums go to the workspace and a second launch adds them in a fixed order:
+// deterministic, no atomics.  dZ enters the sums unrounded.
+#include <algorithm>
+
 #include "activation.cuh"
 #include "internal.h"
 
@@ -29,66 +34,117 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 constexpr int AB_THREADS = 256;
+constexpr int AB_ROWS = 4;  // rows a thread loads together
 
-// blockIdx.y: block of `rows` rows; blockIdx.x: 8 AB_THREADS columns.  Outputs may be the inputs'
-// own buffers (every element is read before it is written, by one thread).
+// blockIdx.y: block of `rows` rows; blockIdx.x: cw (a power of two) column vectors.
 template <int ACT, bool GATED>
 __global__ void __launch_bounds__(AB_THREADS) act_backward_kernel(const uint4* dY, const uint4* Z, const uint4* U,
-                                                                  int64_t M, int64_t N8, int64_t rows, uint4* dZ,
+                                                                  int64_t M, int64_t N8, int64_t rows, int cw, uint4* dZ,
                                                                   uint4* dU, float* part) {
-    const int64_t c = (int64_t)blockIdx.x * AB_THREADS + threadIdx.x;
-    if (c >= N8) return;
+    const int rl = AB_THREADS / cw, lane = threadIdx.x / cw;
+    const int64_t c = (int64_t)blockIdx.x * cw + threadIdx.x % cw;
     const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = m0 + rows < M ? m0 + rows : M;
     float sum[8] = {};
-    for (int64_t m = m0; m < m1; ++m) {
-        const int64_t e = m * N8 + c;
-        float dy[8], z[8] = {}, u[8], dz[8], du[8];
-        unpack8(dY[e], dy);
-        if (Z) unpack8(Z[e], z);
-        if (GATED) unpack8(U[e], u);
+    if (c < N8) {
+        for (int64_t mb = m0 + lane; mb < m1; mb += (int64_t)AB_ROWS * rl) {
+            uint4 vy[AB_ROWS], vz[AB_ROWS] = {}, vu[AB_ROWS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float a;
-            const float d = act_grad<ACT>(z[i], a);
-            if (GATED) {
-                dz[i] = dy[i] * u[i] * d;
-                du[i] = dy[i] * a;
-            } else {
-                dz[i] = dy[i] * d;
-                sum[i] += dz[i];
+            for (int i = 0; i < AB_ROWS; ++i) {
+                const int64_t m = mb + (int64_t)i * rl;
+                if (m < m1) {
+                    vy[i] = dY[m * N8 + c];
+                    if (Z) vz[i] = Z[m * N8 + c];
+                    if (GATED) vu[i] = U[m * N8 + c];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AB_ROWS; ++i) {
+                const int64_t m = mb + (int64_t)i * rl;
+                if (m >= m1) break;
+                float dy[8], z[8], u[8], dz[8], du[8];
+                unpack8(vy[i], dy);
+                unpack8(vz[i], z);
+                if (GATED) unpack8(vu[i], u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float a;
+                    const float d = act_grad<ACT>(z[j], a);
+                    if (GATED) {
+                        dz[j] = dy[j] * u[j] * d;
+                        du[j] = dy[j] * a;
+                    } else {
+                        dz[j] = dy[j] * d;
+                        sum[j] += dz[j];
+                    }
+                }
+                if (dZ) dZ[m * N8 + c] = pack8(dz);
+                if (GATED) dU[m * N8 + c] = pack8(du);
             }
         }
-        if (dZ) dZ[e] = pack8(dz);
-        if (GATED) dU[e] = pack8(du);
     }
-    if (!GATED && part) {
-        float4* p = reinterpret_cast<float4*>(part + ((int64_t)blockIdx.y * N8 + c) * 8);
-        p[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-        p[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+    if (!GATED && part) {  // uniform over the grid
+        __shared__ float sh[AB_THREADS][9];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sh[threadIdx.x][j] = sum[j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < cw * 8; i += AB_THREADS) {  // column i % 8 of vector i / 8
+            const int64_t cc = (int64_t)blockIdx.x * cw + i / 8;
+            if (cc >= N8) continue;
+            float s = 0.0f;
+            for (int l = 0; l < rl; ++l) s += sh[l * cw + i / 8][i % 8];
+            part[((int64_t)blockIdx.y * N8 + cc) * 8 + i % 8] = s;
+        }
     }
 }
 
+// dbias[n] = sum of the row blocks' partials: eight threads of a column take every eighth block, then
+// their sums are added in order.  A programmatic dependent of the kernel that writes the partials.
 __global__ void __launch_bounds__(AB_THREADS) column_sum_kernel(const float* part, int64_t blocks, int64_t N, float* dbias) {
-    const int64_t n = (int64_t)blockIdx.x * AB_THREADS + threadIdx.x;
-    if (n >= N) return;
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ float sh[8][32];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t n = (int64_t)blockIdx.x * 32 + x;
     float s = 0.0f;
-    for (int64_t b = 0; b < blocks; ++b) s += part[b * N + n];
-    dbias[n] = s;
+    if (n < N)
+        for (int64_t b = y; b < blocks; b += 8) s += part[b * N + n];
+    sh[y][x] = s;
+    __syncthreads();
+    if (y == 0 && n < N) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sh[i][x];
+        dbias[n] = s;
+    }
 }
 
-// Rows per CTA and row blocks: a function of M alone, so that the workspace size needs no device.
-int64_t ab_rows(int64_t M) { return M <= 4096 ? 16 : (M + 255) / 256; }
-int64_t ab_blocks(int64_t M) { return (M + ab_rows(M) - 1) / ab_rows(M); }
+// The launch shape, a function of M and N alone (the workspace query needs no device).
+struct AbPlan {
+    int cw;
+    int64_t rows, blocks;
+};
+AbPlan ab_plan(int64_t M, int64_t N) {
+    AbPlan p;
+    p.cw = 1;
+    while (p.cw < AB_THREADS && p.cw < N / 8) p.cw *= 2;
+    const int64_t rl = AB_THREADS / p.cw;
+    // 16 rows a thread, more where that would be over 512 row blocks (their sums are read again)
+    p.rows = rl * std::max<int64_t>(16, (M + 512 * rl - 1) / (512 * rl));
+    p.blocks = (M + p.rows - 1) / p.rows;
+    return p;
+}
 
 }  // namespace
 
-size_t act_backward_workspace(int64_t M, int64_t N) { return (size_t)ab_blocks(M) * (size_t)N * 4; }
+size_t act_backward_workspace(int64_t M, int64_t N) {
+    return M == 0 || N == 0 ? 0 : (size_t)ab_plan(M, N).blocks * (size_t)N * 4;
+}
 
 cudaError_t launch_act_backward(const uint16_t* dY, const uint16_t* Z, const uint16_t* U, int64_t M, int64_t N,
                                 int activation, uint16_t* dZ, uint16_t* dU, float* dbias, void* ws,
                                 cudaStream_t stream) {
+    const AbPlan pl = ab_plan(M, N);
     const int64_t N8 = N / 8;
-    const dim3 grid((unsigned)((N8 + AB_THREADS - 1) / AB_THREADS), (unsigned)ab_blocks(M));
+    const dim3 grid((unsigned)((N8 + pl.cw - 1) / pl.cw), (unsigned)pl.blocks);
     float* part = dbias ? static_cast<float*>(ws) : nullptr;
     auto p = [](const uint16_t* q) { return reinterpret_cast<const uint4*>(q); };
     auto o = [](uint16_t* q) { return reinterpret_cast<uint4*>(q); };
@@ -96,16 +152,23 @@ cudaError_t launch_act_backward(const uint16_t* dY, const uint16_t* Z, const uin
         constexpr int ACT = decltype(act)::value;
         if (U)
             act_backward_kernel<ACT, true>
-                <<<grid, AB_THREADS, 0, stream>>>(p(dY), p(Z), p(U), M, N8, ab_rows(M), o(dZ), o(dU), nullptr);
+                <<<grid, AB_THREADS, 0, stream>>>(p(dY), p(Z), p(U), M, N8, pl.rows, pl.cw, o(dZ), o(dU), nullptr);
         else
             act_backward_kernel<ACT, false>
-                <<<grid, AB_THREADS, 0, stream>>>(p(dY), p(Z), p(U), M, N8, ab_rows(M), o(dZ), o(dU), part);
+                <<<grid, AB_THREADS, 0, stream>>>(p(dY), p(Z), p(U), M, N8, pl.rows, pl.cw, o(dZ), o(dU), part);
         return cudaGetLastError();
     });
     if (e != cudaSuccess || !dbias) return e;
-    column_sum_kernel<<<(unsigned)((N + AB_THREADS - 1) / AB_THREADS), AB_THREADS, 0, stream>>>(part, ab_blocks(M), N,
-                                                                                               dbias);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((N + 31) / 32), 1, 1);
+    cfg.blockDim = dim3(AB_THREADS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, column_sum_kernel, (const float*)part, pl.blocks, N, dbias);
 }
 
 }  // namespace w4

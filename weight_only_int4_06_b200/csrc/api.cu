@@ -572,11 +572,14 @@ static cudaError_t zero_half(uint16_t* p, int64_t rows, int64_t cols, cudaStream
     return rows == 0 || cols == 0 ? cudaSuccess : cudaMemsetAsync(p, 0, (size_t)rows * (size_t)cols * 2, s);
 }
 
-// The GEMV up to 16 activation rows where it serves the shape and can bulk-copy the metadata, else the
-// tensor-core product.
+// The GEMV up to 8 activation rows where one launch serves the shape and can bulk-copy the metadata,
+// else the tensor-core product.  Measured on B200 (us, residual epilogue, graph of back-to-back calls),
+// GEMV vs tensor cores: M = 8, K = 4096, N = 11008 14.7 vs 20.4; K = 28672, N = 8192 41 vs 59; but M = 8,
+// K = 11008, N = 4096 in two launches of 4 rows 24.4 vs 19.4; M = 16 at those shapes 20.7 vs 20.4, 82 vs
+// 59 and 47.9 vs 19.4.
 static bool ffn_decode(int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2) {
     auto meta_ok = [](const W4Layer& l) { return aligned16(l.scales) && aligned16(l.zeros); };
-    return meta_ok(w) && (!w2 || meta_ok(*w2)) && decode_ffn_rows(M, N, K, w2 != nullptr) > 0;
+    return meta_ok(w) && (!w2 || meta_ok(*w2)) && decode_ffn_fits(M, N, K, w2 != nullptr);
 }
 
 static cudaError_t launch_ffn(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,

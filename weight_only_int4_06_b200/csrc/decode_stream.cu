@@ -781,10 +781,10 @@ static cudaError_t ds_launch_mt(const CUtensorMap& tm, const CUtensorMap& tmS, c
         case 4: return launch(std::integral_constant<int, 4>{}, I32{});
         case 8: return launch(std::integral_constant<int, 8>{}, I32{});
         default:
-            if constexpr (KS)
+            if constexpr (KS && EPI == 0)
                 return launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
             else
-                return cudaErrorInvalidValue;  // the 16-row instantiation runs in split mode only
+                return cudaErrorInvalidValue;  // the 16-row instantiation: split mode, no epilogue
     }
 }
 
@@ -835,70 +835,42 @@ cudaError_t launch_decode_stream(const uint16_t* X, int64_t M, int64_t N, int64_
 }
 
 // ---------------------------------------------------------------- with an epilogue (w4_gemm_fused, w4_gemm_gated)
-// Activation rows per launch: the plain GEMV's where they fit, else fewer (long K whose groups cannot
-// be sliced); 0: the shape is not served.
-int64_t decode_ffn_rows(int64_t M, int64_t N, int64_t K, bool gated) {
-    if (M > DS_MAXM || (gated && K % 256 != 0)) return 0;
+bool decode_ffn_fits(int64_t M, int64_t N, int64_t K, bool gated) {
     DecodePlan p;
-    for (int64_t rows : std::initializer_list<int64_t>{decode_stream_rows(M, K), 4, 2, 1})
-        if (plan_decode_stream(std::min(M, rows), gated ? 2 * N : N, K, &p)) return rows;
-    return 0;
-}
-
-int64_t decode_ffn_launches(int64_t M, int64_t N, int64_t K, bool gated) {
-    const int64_t rows = decode_ffn_rows(M, N, K, gated);
-    return rows ? (M + rows - 1) / rows : 0;
+    return M <= 8 && (!gated || K % 256 == 0) && plan_decode_stream(M, gated ? 2 * N : N, K, &p);
 }
 
 size_t decode_ffn_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
-    const int64_t rows = decode_ffn_rows(M, N, K, gated);
-    size_t need = 0;
-    if (rows == 0) return 0;
-    for (int64_t mc : std::initializer_list<int64_t>{std::min(M, rows), M % rows}) {
-        if (mc < 1) continue;
-        const int ks = decode_stream_slices(mc, K);
-        if (ks > 1) need = std::max(need, (size_t)ks * (size_t)mc * (size_t)N * (gated ? 8 : 4));
-    }
-    return need;
+    if (!decode_ffn_fits(M, N, K, gated)) return 0;
+    const int ks = decode_stream_slices(M, K);
+    return ks > 1 ? (size_t)ks * (size_t)M * (size_t)N * (gated ? 8 : 4) : 0;
 }
 
 cudaError_t launch_decode_ffn(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
                               const W4Epilogue& ep, void* ws, bool weights_static, int* status, cudaStream_t stream) {
-    const int64_t rows = decode_ffn_rows(M, N, K, w2 != nullptr);
-    if (rows == 0) return cudaErrorInvalidValue;
-    auto at = [](const uint16_t* q, int64_t o) { return q ? const_cast<uint16_t*>(q) + o : nullptr; };
-    auto hf = [](const uint16_t* q) { return reinterpret_cast<__half*>(const_cast<uint16_t*>(q)); };
-    for (int64_t m0 = 0; m0 < M; m0 += rows) {
-        const int64_t mc = std::min(rows, M - m0), o = m0 * N;
-        DecodePlan p;
-        if (!plan_decode_stream(mc, w2 ? 2 * N : N, K, &p)) return cudaErrorInvalidValue;
-        const bool split = p.ncs > 0 && p.ks > 1;
-        if (split && !ws) return cudaErrorInvalidValue;
-        float* P = split ? static_cast<float*>(ws) : nullptr;
-        W4Epilogue e1 = ep;
-        e1.residual = at(ep.residual, o);
-        e1.Y = at(ep.Y, o);
-        e1.Z = at(ep.Z, o);
-        e1.U = at(ep.U, o);
-        cudaError_t e;
-        if (w2) {
-            DsExtra<2> ex = {};
-            if (!ds_maps(p, w2->packed, w2->scales, w2->zeros, N, K, 8, &ex.tmW2, &ex.tmS2, &ex.tmZ2))
-                return cudaErrorInvalidValue;
-            ex.scales2 = w2->scales;
-            ex.zeros2 = w2->zeros;
-            ex.G = hf(e1.Z);
-            ex.U = hf(e1.U);
-            ex.act = ep.activation;
-            e = ds_run<2>(p, X + m0 * K, mc, N, K, w.packed, w.scales, w.zeros, e1.Y, P, weights_static, status, stream, ex);
-        } else {
-            const DsExtra<1> ex = {hf(ep.bias), hf(e1.residual), hf(e1.Z), ep.activation};
-            e = ds_run<1>(p, X + m0 * K, mc, N, K, w.packed, w.scales, w.zeros, e1.Y, P, weights_static, status, stream, ex);
-        }
-        if (e != cudaSuccess) return e;
-        if (split && (e = launch_ffn_reduce(P, p.ks, mc, N, w2 != nullptr, e1, stream)) != cudaSuccess) return e;
+    DecodePlan p;
+    if (!plan_decode_stream(M, w2 ? 2 * N : N, K, &p)) return cudaErrorInvalidValue;
+    const bool split = p.ncs > 0 && p.ks > 1;
+    if (split && !ws) return cudaErrorInvalidValue;
+    float* P = split ? static_cast<float*>(ws) : nullptr;
+    cudaError_t e;
+    if (w2) {
+        DsExtra<2> ex = {};
+        if (!ds_maps(p, w2->packed, w2->scales, w2->zeros, N, K, 8, &ex.tmW2, &ex.tmS2, &ex.tmZ2))
+            return cudaErrorInvalidValue;
+        ex.scales2 = w2->scales;
+        ex.zeros2 = w2->zeros;
+        ex.G = reinterpret_cast<__half*>(ep.Z);
+        ex.U = reinterpret_cast<__half*>(ep.U);
+        ex.act = ep.activation;
+        e = ds_run<2>(p, X, M, N, K, w.packed, w.scales, w.zeros, ep.Y, P, weights_static, status, stream, ex);
+    } else {
+        const DsExtra<1> ex = {reinterpret_cast<const __half*>(ep.bias), reinterpret_cast<const __half*>(ep.residual),
+                               reinterpret_cast<__half*>(ep.Z), ep.activation};
+        e = ds_run<1>(p, X, M, N, K, w.packed, w.scales, w.zeros, ep.Y, P, weights_static, status, stream, ex);
     }
-    return cudaSuccess;
+    if (e != cudaSuccess || !split) return e;
+    return launch_ffn_reduce(P, p.ks, M, N, w2 != nullptr, ep, stream);
 }
 
 }  // namespace w4

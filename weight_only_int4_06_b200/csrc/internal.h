@@ -235,10 +235,9 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
 // The epilogue of the sum of `slices` partial products P [slice][layer][M][N], in slice order.
 cudaError_t launch_ffn_reduce(const float* P, int slices, int64_t M, int64_t N, bool gated, const W4Epilogue& ep,
                               cudaStream_t stream);
-// decode_stream.cu, M <= 16: the same through the GEMV.  Rows per launch (0: the shape is not served;
-// scales and zeros must be 16-byte aligned); ws: decode_ffn_workspace bytes.
-int64_t decode_ffn_rows(int64_t M, int64_t N, int64_t K, bool gated);
-int64_t decode_ffn_launches(int64_t M, int64_t N, int64_t K, bool gated);
+// decode_stream.cu: the same through one GEMV launch (M <= 8; scales and zeros 16-byte aligned), where
+// decode_ffn_fits; ws: decode_ffn_workspace bytes.
+bool decode_ffn_fits(int64_t M, int64_t N, int64_t K, bool gated);
 size_t decode_ffn_workspace(int64_t M, int64_t N, int64_t K, bool gated);
 cudaError_t launch_decode_ffn(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
                               const W4Epilogue& ep, void* ws, bool weights_static, int* status, cudaStream_t stream);

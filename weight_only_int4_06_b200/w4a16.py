@@ -96,7 +96,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _check(st: int, where: str):
-    if st != W4_OK:
+    if st:  # W4_OK is 0
         raise W4Error(st, where)
 
 
@@ -618,7 +618,7 @@ def awq_clip_search(X: torch.Tensor, W: torch.Tensor, act_scale: torch.Tensor | 
 # ------------------------------------------------------------------ feed-forward operators
 def _arg(t: torch.Tensor, dtype, shape, dev, name) -> int:
     """Device address of a tensor argument, its type, shape, device and layout checked."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():  # dev: a GPU
         return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -639,6 +639,11 @@ def _matrix(t: torch.Tensor, name: str):
 
 def _layer_args(packed, scales, zeros, N: int, K: int, group: int, dev, name: str):
     meta = (N, K // group if group > 0 else 0)
+    if (packed.dtype is torch.int32 and scales.dtype is torch.float16 and zeros.dtype is torch.uint8
+            and packed.shape == (N, K // 8) and scales.shape == meta and zeros.shape == meta
+            and packed.device == dev and scales.device == dev and zeros.device == dev
+            and packed.is_contiguous() and scales.is_contiguous() and zeros.is_contiguous()):
+        return packed.data_ptr(), scales.data_ptr(), zeros.data_ptr()
     return (_arg(packed, torch.int32, (N, K // 8), dev, name + "packed"),
             _arg(scales, torch.float16, meta, dev, name + "scales"),
             _arg(zeros, torch.uint8, meta, dev, name + "zeros"))
@@ -650,7 +655,7 @@ def _other_context(dev, stream):
     as short as their launch); else the context to allocate and launch in, so that new outputs and
     workspaces belong to `stream`."""
     if stream is None:
-        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return None if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream, device=dev)
     if stream.device != dev:
