@@ -54,22 +54,24 @@ constexpr uint32_t FG_P_BYTES = 128 * 64;          // packed codes of one group:
 constexpr uint32_t FG_SMEM = 227 * 1024;
 constexpr uint32_t FG_EPI = 32 * 128 * 4;          // a fold warpgroup's 32 rows of 128 fp32
 
-// NMAX columns at most.  192 (large batches): 96 accumulators per fold thread.  64 (small ones): twice
-// the dequantising warps, which bound it, and twice the TMEM buffers.  Every thread launches with
-// kRegs registers; the fold warps take what the others give up (in warpgroup shares: 24 + 2 x 64 + 2 x
-// 160 = 472 of 5 x 96, and 24 + 4 x 64 + 2 x 112 = 504 of 7 x 72).
+// NMAX columns at most.
+// 256 (large batches): the dequantised groups lie in shared memory (K-major, 128-byte swizzle).
+// 64 (small batches): in tensor memory, and four warpgroups dequantise, which bounds it.
+// Every thread launches with kRegs registers; the fold warps take what the others give up (in
+// warpgroup shares: 24 + 80 + 2 x 200 = 504 of 4 x 128, and 24 + 4 x 64 + 2 x 112 = 504 of 7 x 72).
 template <int NMAX>
 struct FgCfg {
     static constexpr bool kWide = NMAX > 64;
-    static constexpr int kSubs = kWide ? 2 : 1;     // products a group is issued as (tn / kSubs columns each)
-    static constexpr int kDW = kWide ? 2 : 4;       // dequantising warpgroups
+    static constexpr int kDW = kWide ? 1 : 4;       // dequantising warpgroups
     static constexpr int kNB = kWide ? 2 : 4;       // TMEM buffers of group sums
-    static constexpr int kAG = kWide ? 2 : 4;       // dequantised groups in TMEM (64 columns each)
+    static constexpr int kAG = kWide ? 2 : 4;       // dequantised groups
     static constexpr int kThreads = 128 * (1 + kDW + 2);
-    static constexpr uint32_t kACol = kNB * NMAX;   // 384 or 256; + 64 kAG = 512
-    static constexpr int kRegs = kWide ? 96 : 72;
-    static constexpr int kRegsMisc = 24, kRegsDeq = 64, kRegsFold = kWide ? 160 : 112;
+    static constexpr uint32_t kACol = kNB * NMAX;   // 64: first TMEM column of the dequantised groups (64 each)
+    static constexpr uint32_t kWBytes = kWide ? 128 * 128 * 2 : 0;  // 256: shared memory of one
+    static constexpr int kRegs = kWide ? 128 : 72;
+    static constexpr int kRegsMisc = 24, kRegsDeq = kWide ? 80 : 64, kRegsFold = kWide ? 200 : 112;
     static_assert(kRegsMisc + kDW * kRegsDeq + 2 * kRegsFold <= (3 + kDW) * kRegs, "register shares");
+    static_assert(kNB * NMAX + (kWide ? 0 : 64 * kAG) <= 512, "TMEM");
 };
 
 struct FgArgs {
@@ -233,7 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     const __grid_constant__ CUtensorMap tmW1, const FgArgs p) {
     using C = FgCfg<NMAX>;
     constexpr int NACC = NMAX / 2;            // columns per fold thread
-    constexpr int NB = C::kNB, AG = C::kAG, GS = C::kDW, SUBS = C::kSubs;
+    constexpr int NB = C::kNB, AG = C::kAG, GS = C::kDW;
     constexpr int FOLD_WARP = 4 + 4 * C::kDW;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_align1024(smem_raw);
@@ -244,27 +246,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
     const int S = p.stages;
     const uint32_t xbytes = (uint32_t)p.tn * 128u;  // tn/2 rows x 128 k x 2 bytes
     const uint32_t stage_bytes = xbytes + FG_P_BYTES;
-    const uint32_t epi0 = (uint32_t)S * stage_bytes;  // the epilogue's staging rows, then the barriers
+    const uint32_t w0 = (uint32_t)S * stage_bytes;    // dequantised groups, the epilogue's staging rows, the barriers
+    const uint32_t epi0 = w0 + AG * C::kWBytes;
     const uint32_t bar0 = sbase + epi0 + 2 * FG_EPI;
     auto full_bar = [&](int s) { return bar0 + 8 * s; };
     auto done_bar = [&](int s) { return bar0 + 8 * (FG_MAXS + s); };
     auto a_full = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + i); };
     auto d_empty = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + 4 + i); };
-    auto d_full = [&](int i) { return bar0 + 8 * (2 * FG_MAXS + 8 + i); };
-    unsigned char* tail = smem + epi0 + 2 * FG_EPI + 8 * (2 * FG_MAXS + 12);
+    unsigned char* tail = smem + epi0 + 2 * FG_EPI + 8 * (2 * FG_MAXS + 8);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(done_bar(s), SUBS);
+            mbar_init(done_bar(s), 1);
         }
         for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 8);    // a dequantising warpgroup of each CTA
-        for (int i = 0; i < SUBS * NB; ++i) {
-            mbar_init(d_empty(i), 16 / SUBS);  // eight warps of each CTA, or the four that fold this product
-            mbar_init(d_full(i), 1);
-        }
+        for (int i = 0; i < NB; ++i) mbar_init(d_empty(i), 16);  // eight fold warps of each CTA
         *abort_flag = 0;
         fence_mbarrier_init();
         prefetch_tmap(&tmX);
@@ -325,8 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
-                const int part = p.tn / (2 * SUBS);  // X rows of one product in this CTA
-                const int mx = w.m0 + (int)rank * part;
+                const int mx = w.m0 + (int)rank * (p.tn / 2);
                 for (int g = w.g0; g < w.g1; ++g, ++it) {
                     if (it >= ahead && !mbar_wait_bounded(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
                     if (elect_one()) {
@@ -335,12 +333,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                             mbar_arrive_expect_tx(full_bar(s), stage_bytes);
                             load_w(w, g, s);
                         }
-#pragma unroll
-                        for (int f = 0; f < SUBS; ++f) {
-                            const uint32_t xf = xs + (uint32_t)f * (xbytes / 4);
-                            tma_load_2d(xf, &tmX, g * 128, mx + 2 * f * part, full_bar(s));
-                            tma_load_2d(xf + xbytes / 2, &tmX, g * 128 + 64, mx + 2 * f * part, full_bar(s));
-                        }
+                        tma_load_2d(xs, &tmX, g * 128, mx, full_bar(s));
+                        tma_load_2d(xs + xbytes / 2, &tmX, g * 128 + 64, mx, full_bar(s));
                     }
                     __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
@@ -352,17 +346,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 mbar_wait_bounded(full_bar(i % S), (uint32_t)(i / S) & 1, nullptr, 200000000ull);
                 if (ok) mbar_wait_bounded(done_bar(i % S), (uint32_t)(i / S) & 1, abort_flag);
             }
-        } else if ((warp == 1 || (SUBS == 2 && warp == 3)) && rank == 0) {
-            // -------------------------------------------------------- MMA issuers (for both CTAs)
-            const int f = SUBS == 2 ? warp >> 1 : 0;  // which of the group's products
-            const uint32_t idesc = idesc_f16_f32(256, p.tn / SUBS);
+        } else if (warp == 1 && rank == 0) {
+            // -------------------------------------------------------- MMA issuer (for both CTAs)
+            const uint32_t idesc = idesc_f16_f32(256, p.tn);
             pdl_wait();
             int it = 0, s = 0;
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
                 for (int g = w.g0; g < w.g1; ++g, ++it) {
-                    const int b = f * NB + it % NB, a = it % AG;
+                    const int b = it % NB, a = it % AG;
                     if (!mbar_wait_bounded(d_empty(b), ((uint32_t)(it / NB) & 1) ^ 1, abort_flag) ||
                         !mbar_wait_bounded(a_full(a), (uint32_t)(it / AG) & 1, abort_flag)) {
                         fail();
@@ -371,13 +364,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     }
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes + (uint32_t)f * (xbytes / 4));
+                        const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes);
+                        const uint64_t ad = sw128_kmajor_desc(sbase + w0 + (uint32_t)a * C::kWBytes);
                         const uint64_t half = (uint64_t)(xbytes / 2) >> 4;  // the second 64 k
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            mma_f16_ts_pair(tmem + b * (NMAX / SUBS), tmem + C::kACol + a * 64 + j * 8,
-                                            bd + (j >> 2) * half + 2 * (j & 3), idesc, j != 0);
-                        if (SUBS == 2) tc_commit_pair(d_full(b));
+                        for (int j = 0; j < 8; ++j) {
+                            const uint64_t bj = bd + (j >> 2) * half + 2 * (j & 3);
+                            if constexpr (C::kWide)
+                                mma_f16_ss_pair(tmem + b * NMAX, ad + (j >> 2) * (C::kWBytes / 2 >> 4) + 2 * (j & 3), bj, idesc,
+                                                j != 0);
+                            else
+                                mma_f16_ts_pair(tmem + b * NMAX, tmem + C::kACol + a * 64 + j * 8, bj, idesc, j != 0);
+                        }
                         tc_commit_pair(done_bar(s));
                     }
                     __syncwarp();
@@ -385,15 +383,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 }
             }
             // on an abort nobody else waits for what was issued: the pair's TMEM is freed after it
-            if (!ok && it > 0 && SUBS == 1)
-                mbar_wait_bounded(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
-            if (!ok && it > 0 && SUBS == 2)
-                mbar_wait_bounded(d_full(f * NB + (it - 1) % NB), (uint32_t)((it - 1) / NB) & 1, nullptr, 200000000ull);
+            if (!ok && it > 0) mbar_wait_bounded(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
         }
     } else if (warp < FOLD_WARP) {
         regs_dec<C::kRegsDeq>();
         // ------------------------------------------------------------ dequantisation
-        static_assert(GS == AG, "each warpgroup has its own slot");
         const int wg = (warp - 4) >> 2, q = warp & 3;  // this warpgroup's groups: wg, wg + GS, ...
         const int r = q * 32 + lane;  // row of the CTA's 128 = TMEM lane
         const uint32_t sw = (uint32_t)(r >> 1) & 3;  // 64-byte TMA swizzle
@@ -433,51 +427,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 // q - z = (1024 + q) - (1024 + z) from a low nibble, (1024 + 16 q) / 16 - (64 + z) from a
                 // high one: exact
                 const uint32_t zl = (0x6400u + z) * 0x10001u, zh = (0xD400u | (z << 4)) * 0x10001u;
+                const uint32_t slot = (uint32_t)(it % AG);
+                // the group that used this slot AG groups ago has been multiplied
+                auto free_slot = [&]() {
+                    if (it >= AG) {
+                        if (ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
+                        sa += GS;
+                        if (sa >= S) { sa -= S; pa ^= 1; }
+                    }
+                };
+                auto dequant = [&](uint32_t wd, uint32_t (&o)[4]) {
+                    const uint32_t w8 = wd >> 8;
+                    const uint32_t lo0 = hsub2_u32(lop3_and_or(wd, 0x000F000Fu, 0x64006400u), zl);              // k0, k4
+                    const uint32_t hi0 = hfma2_u32(lop3_and_or(wd, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k1, k5
+                    const uint32_t lo1 = hsub2_u32(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), zl);              // k2, k6
+                    const uint32_t hi1 = hfma2_u32(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k3, k7
+                    o[0] = __byte_perm(lo0, hi0, 0x5410);  // k0, k1
+                    o[1] = __byte_perm(lo1, hi1, 0x5410);  // k2, k3
+                    o[2] = __byte_perm(lo0, hi0, 0x7632);  // k4, k5
+                    o[3] = __byte_perm(lo1, hi1, 0x7632);  // k6, k7
+                };
                 if (!loaded) {
                     if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
                     load(0, wa, wb);
                 }
                 loaded = false;
-                const uint32_t slot = (uint32_t)(it % AG);
+                if constexpr (C::kWide) {
+                    uint4 wc, wd;
+                    load(1, wc, wd);
+                    free_slot();
+                    const uint32_t words[16] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w,
+                                                wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
+                    unsigned char* row = smem + w0 + slot * C::kWBytes + (uint32_t)r * 128;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t words[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-                    uint32_t o[32];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t wd = words[c], w8 = wd >> 8;
-                        const uint32_t lo0 = hsub2_u32(lop3_and_or(wd, 0x000F000Fu, 0x64006400u), zl);              // k0, k4
-                        const uint32_t hi0 = hfma2_u32(lop3_and_or(wd, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k1, k5
-                        const uint32_t lo1 = hsub2_u32(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), zl);              // k2, k6
-                        const uint32_t hi1 = hfma2_u32(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k3, k7
-                        o[4 * c + 0] = __byte_perm(lo0, hi0, 0x5410);  // k0, k1
-                        o[4 * c + 1] = __byte_perm(lo1, hi1, 0x5410);  // k2, k3
-                        o[4 * c + 2] = __byte_perm(lo0, hi0, 0x7632);  // k4, k5
-                        o[4 * c + 3] = __byte_perm(lo1, hi1, 0x7632);  // k6, k7
+                    for (int c = 0; c < 16; ++c) {  // 8-k chunk: block of 64 k, chunk in the row's 128 bytes
+                        uint32_t o[4];
+                        dequant(words[c], o);
+                        *reinterpret_cast<uint4*>(row + (c >> 3) * (C::kWBytes / 2) + (((c & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
                     }
-                    if (h == 0) {
-                        load(1, wa, wb);
-                        if (it >= AG) {  // the group that used these columns AG groups ago has been multiplied
-                            if (ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
-                            sa += GS;
-                            if (sa >= S) { sa -= S; pa ^= 1; }
-                        }
-                    }
-                    if (ok) tmem_st_32x32b_x32(taddr + slot * 64 + h * 32, o);
-                }
-                it += GS;
-                s += GS;
-                if (s >= S) { s -= S; ph ^= 1; }
-                // the next group's codes, where they have arrived, are read while this one's are stored
-                if (ok && g + GS < w.g1 && __all_sync(0xffffffffu, mbar_test(full_bar(s), ph))) {
-                    load(0, wa, wb);
-                    loaded = true;
-                }
-                if (ok) {
-                    tmem_wait_st();
-                    tc_fence_before();
+                    fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor cores
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(remote + 8u * slot);
+                    if (ok && lane == 0) mbar_arrive_cluster(remote + 8u * slot);
+                    it += GS;
+                    s += GS;
+                    if (s >= S) { s -= S; ph ^= 1; }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t words[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                        uint32_t o[32];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o4[4];
+                            dequant(words[c], o4);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[4 * c + j] = o4[j];
+                        }
+                        if (h == 0) {
+                            load(1, wa, wb);
+                            free_slot();
+                        }
+                        if (ok) tmem_st_32x32b_x32(taddr + slot * 64 + h * 32, o);
+                    }
+                    it += GS;
+                    s += GS;
+                    if (s >= S) { s -= S; ph ^= 1; }
+                    // the next group's codes, where they have arrived, are read while this one's are stored
+                    if (ok && g + GS < w.g1 && __all_sync(0xffffffffu, mbar_test(full_bar(s), ph))) {
+                        load(0, wa, wb);
+                        loaded = true;
+                    }
+                    if (ok) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(remote + 8u * slot);
+                    }
                 }
             }
             skip = g - w.g1;
@@ -490,11 +516,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
         const int ncol = p.tn / 2;
         const bool upper = lane >= 16;
         const unsigned short* sbase_row = GATED && upper ? p.s1 : p.s0;
-        const uint32_t remote = map_shared(d_empty(SUBS == 2 ? f * NB : 0), 0);
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(SUBS == 2 ? f * NB * NACC : f * ncol);
+        const uint32_t remote = map_shared(d_empty(0), 0);
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(f * ncol);
         pdl_wait();  // the outputs may be read, the residual written, by the preceding kernel
         bool ok = true;
-        int b = 0, s = 0;  // TMEM buffer and, with one product a group, ring stage of the group
+        int b = 0, s = 0;  // TMEM buffer and ring stage of the group
         uint32_t ph = 0;
         for (int u = cluster; u < p.units; u += n_clusters) {
             const FgUnit w = fg_unit(p, u);
@@ -510,13 +536,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 if (((g & 3) == 0 || g == w.g0) && nv && (g & ~3) + 4 < p.G) s4n = fg_scales4(srow, (g & ~3) + 4, p.G, p.vec);
                 const float sc = __half2float(__ushort_as_half((unsigned short)(s4 >> (16 * (g & 3)))));
                 const uint64_t sc2 = pack_f32x2(__float_as_uint(sc), __float_as_uint(sc));
-                if (ok && !warp_wait(SUBS == 2 ? d_full(f * NB + b) : done_bar(s), ph, abort_flag)) { fail(); ok = false; }
-                if (SUBS == 1 && ++s == S) { s = 0; ph ^= 1; }
+                if (ok && !warp_wait(done_bar(s), ph, abort_flag)) { fail(); ok = false; }
+                if (++s == S) { s = 0; ph ^= 1; }
                 if (ok) {
                     tc_fence_after();
-                    const uint32_t src = taddr + (uint32_t)(b * (SUBS == 2 ? NACC : NMAX));
-                    // rounds of 48 or 32 columns, each one wait (columns past tn hold old sums: never stored)
-                    constexpr int RC = NACC >= 48 && GATED ? 48 : 32;
+                    const uint32_t src = taddr + (uint32_t)(b * NMAX);
+                    // rounds of 32 columns, each one wait (columns past tn hold old sums: never stored)
+                    constexpr int RC = 32;
 #pragma unroll
                     for (int c = 0; c < NACC; c += RC) {
                         if (c < ncol) {
@@ -539,10 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                         }
                     }
                 }
-                if (++b == NB) {
-                    b = 0;
-                    if (SUBS == 2) ph ^= 1;
-                }
+                if (++b == NB) b = 0;
             }
             if (wg_barrier_any(1 + f, !ok)) continue;  // all four warps agree before the staging barriers
             const int m0 = w.m0 + f * ncol;
@@ -619,7 +642,7 @@ __global__ void __launch_bounds__(256) ffn_reduce_kernel(const float* P, int sli
 
 struct FgPlan {
     int tn, ks, stages, m_tiles, n_tiles, units;
-    bool wide;  // the 192-column instantiation
+    bool wide;  // the 256-column instantiation
     uint32_t smem;
 };
 
@@ -629,8 +652,8 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
     const int64_t n_tiles = (N + rows - 1) / rows;
     FgPlan best = {};
     double best_t = -1.0;
-    for (int tn : {32, 64, 128, 192}) {
-        if (tn > 32 && tn / 2 >= M) break;
+    for (int tn = 32; tn <= 256; tn += 32) {
+        if (tn > 32 && tn >= M + 32) break;
         const int64_t m_tiles = (M + tn - 1) / tn;
         const int64_t tiles = m_tiles * n_tiles;
         for (int ks = 1; ks <= 16 && ks <= G; ++ks) {
@@ -639,7 +662,7 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
             const int64_t waves = (units + pairs - 1) / pairs;
             // cycles per group: the products (4 tn) or the dequantising warps' issue rate; per unit: filling
             // and the epilogue; a second launch and its traffic when K is cut
-            const double group = std::max(4.0 * tn, 380.0);
+            const double group = tn > 64 ? std::max(4.6 * tn, 700.0) : 650.0;
             double t = (double)waves * ((double)((G + ks - 1) / ks) * group + 1500.0 + 8.0 * tn);
             if (ks > 1) t += 4000.0 + (double)ks * (double)M * (double)N * (gated ? 2 : 1) * 8.0 / 3000.0;
             if (best_t < 0.0 || t < best_t) {
@@ -654,8 +677,9 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
     }
     best.wide = best.tn > 64;
     const uint32_t stage = (uint32_t)best.tn * 128u + FG_P_BYTES;
-    best.stages = (int)std::min<uint32_t>((FG_SMEM - 1024 - 512 - 2 * FG_EPI) / stage, FG_MAXS);
-    best.smem = stage * (uint32_t)best.stages + 2 * FG_EPI + 512 + 1024;
+    const uint32_t fixed = (best.wide ? FgCfg<256>::kAG * FgCfg<256>::kWBytes : 0) + 2 * FG_EPI + 512;
+    best.stages = (int)std::min<uint32_t>((FG_SMEM - 1024 - fixed) / stage, FG_MAXS);
+    best.smem = stage * (uint32_t)best.stages + fixed + 1024;
     return best;
 }
 
@@ -732,7 +756,7 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
     if (pl.ks > 1 && !ws) return cudaErrorInvalidValue;
     CUtensorMap tx, t0, t1;
     if (!make_tensor_map_2d(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)K, (uint64_t)M, 64,
-                            (uint32_t)(pl.wide ? pl.tn / 4 : pl.tn / 2),
+                            (uint32_t)(pl.tn / 2),
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     const uint32_t box = gated ? 16 : 128;
@@ -774,8 +798,8 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
     a.early = weights_static ? 1 : 0;
     a.status = status;
     cudaError_t e;
-    if (gated) e = pl.wide ? fg_launch<true, 192>(tx, t0, t1, a, pl, stream) : fg_launch<true, 64>(tx, t0, t1, a, pl, stream);
-    else e = pl.wide ? fg_launch<false, 192>(tx, t0, t1, a, pl, stream) : fg_launch<false, 64>(tx, t0, t1, a, pl, stream);
+    if (gated) e = pl.wide ? fg_launch<true, 256>(tx, t0, t1, a, pl, stream) : fg_launch<true, 64>(tx, t0, t1, a, pl, stream);
+    else e = pl.wide ? fg_launch<false, 256>(tx, t0, t1, a, pl, stream) : fg_launch<false, 64>(tx, t0, t1, a, pl, stream);
     if (e != cudaSuccess || pl.ks == 1) return e;
     return launch_ffn_reduce(a.P, pl.ks, M, N, gated, ep, stream);
 }
