@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(AB_THREADS) act_backward_kernel(const uint4* d
     const int rl = AB_THREADS / cw, lane = threadIdx.x / cw;
     const int64_t c = (int64_t)blockIdx.x * cw + threadIdx.x % cw;
     const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = m0 + rows < M ? m0 + rows : M;
-    float sum[8] = {};
+    F2 sum[4] = {};
     if (c < N8) {
         for (int64_t mb = m0 + lane; mb < m1; mb += (int64_t)AB_ROWS * rl) {
             uint4 vy[AB_ROWS], vz[AB_ROWS] = {}, vu[AB_ROWS];
@@ -66,15 +66,16 @@ __global__ void __launch_bounds__(AB_THREADS) act_backward_kernel(const uint4* d
                 unpack8(vz[i], z);
                 if (GATED) unpack8(vu[i], u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float a;
-                    const float d = act_grad<ACT>(z[j], a);
+                for (int j = 0; j < 8; j += 2) {
+                    F2 a;
+                    const F2 y = f2(dy[j], dy[j + 1]), d = act_grad2<ACT>(f2(z[j], z[j + 1]), a);
                     if (GATED) {
-                        dz[j] = dy[j] * u[j] * d;
-                        du[j] = dy[j] * a;
+                        split(mul2(mul2(y, f2(u[j], u[j + 1])), d), dz[j], dz[j + 1]);
+                        split(mul2(y, a), du[j], du[j + 1]);
                     } else {
-                        dz[j] = dy[j] * d;
-                        sum[j] += dz[j];
+                        const F2 r = mul2(y, d);
+                        sum[j / 2] = add2(sum[j / 2], r);
+                        split(r, dz[j], dz[j + 1]);
                     }
                 }
                 if (dZ) dZ[m * N8 + c] = pack8(dz);
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(AB_THREADS) act_backward_kernel(const uint4* d
     if (!GATED && part) {  // uniform over the grid
         __shared__ float sh[AB_THREADS][9];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sh[threadIdx.x][j] = sum[j];
+        for (int j = 0; j < 8; j += 2) split(sum[j / 2], sh[threadIdx.x][j], sh[threadIdx.x][j + 1]);
         __syncthreads();
         for (int i = threadIdx.x; i < cw * 8; i += AB_THREADS) {  // column i % 8 of vector i / 8
             const int64_t cc = (int64_t)blockIdx.x * cw + i / 8;

@@ -12,7 +12,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // Barrier of one warpgroup.
-__device__ __forceinline__ void wg_barrier(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void wg_barrier(int id) {  // 1 or 2, as constants: an id in a register is slower
+    if (id == 1) asm volatile("bar.sync 1, 128;" ::: "memory");
+    else asm volatile("bar.sync 2, 128;" ::: "memory");
+}
 
 // Whether any of the warpgroup's threads has `bad` set.
 __device__ __forceinline__ bool wg_barrier_any(int id, bool bad) {

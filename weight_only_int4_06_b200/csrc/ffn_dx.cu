@@ -85,11 +85,11 @@ __device__ __forceinline__ void dx_finish(const float (&d)[4], int64_t o, uint2 
         float4_of(gh, g);
         float4_of(uh, u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float a;
-            const float s = act_grad<ACT>(g[j], a);
-            dg[j] = d[j] * u[j] * s;
-            du[j] = d[j] * a;
+        for (int j = 0; j < 4; j += 2) {
+            F2 a;
+            const F2 h = f2(d[j], d[j + 1]), s = act_grad2<ACT>(f2(g[j], g[j + 1]), a);
+            split(mul2(mul2(h, f2(u[j], u[j + 1])), s), dg[j], dg[j + 1]);
+            split(mul2(h, a), du[j], du[j + 1]);
         }
         *reinterpret_cast<uint2*>(out + o) = half4(dg);
         *reinterpret_cast<uint2*>(out2 + o) = half4(du);

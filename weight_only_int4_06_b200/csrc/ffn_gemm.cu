@@ -131,30 +131,72 @@ __device__ __forceinline__ uint32_t fg_zeros4(const uint8_t* row, int g, int G, 
     return v;
 }
 
-// acc (two fp32) += s * v, one packed FMA.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
-}
-__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-
 // 16 columns' sums, ordered before their use by the wait.
 __device__ __forceinline__ void fg_tie(uint32_t (&v)[16]) {
     asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                       "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
 }
 
+// Four neighbouring outputs of a row (element offset o) from their sums.
+template <int ACT, bool GATED>
+__device__ __forceinline__ void fg_finish(const FgArgs& p, const float4& s0, const float4& s1, const uint2& bias, const uint2& res,
+                                          int64_t o) {
+    F2 z[2] = {f2(s0.x, s0.y), f2(s0.z, s0.w)}, y[2];
+    float f[4];
+    if constexpr (GATED) {
+        const F2 u[2] = {f2(s1.x, s1.y), f2(s1.z, s1.w)};
+        y[0] = mul2(act_fwd2<ACT>(z[0]), u[0]);
+        y[1] = mul2(act_fwd2<ACT>(z[1]), u[1]);
+        const float uf[4] = {s1.x, s1.y, s1.z, s1.w};
+        if (p.U) *reinterpret_cast<uint2*>(p.U + o) = half4(uf);
+    } else {
+        if (p.bias) {
+            float4_of(bias, f);
+            z[0] = add2(z[0], f2(f[0], f[1]));
+            z[1] = add2(z[1], f2(f[2], f[3]));
+        }
+        y[0] = act_fwd2<ACT>(z[0]);
+        y[1] = act_fwd2<ACT>(z[1]);
+        if (p.residual) {
+            float4_of(res, f);
+            y[0] = add2(y[0], f2(f[0], f[1]));
+            y[1] = add2(y[1], f2(f[2], f[3]));
+        }
+    }
+    split(y[0], f[0], f[1]);
+    split(y[1], f[2], f[3]);
+    *reinterpret_cast<uint2*>(p.Y + o) = half4(f);
+    if (p.Z) {
+        split(z[0], f[0], f[1]);
+        split(z[1], f[2], f[3]);
+        *reinterpret_cast<uint2*>(p.Z + o) = half4(f);
+    }
+}
+
+// Columns 16 i ... 16 i + 15 of the accumulators (i not a constant) to 16 staged rows.
+template <int NACC, int I = 0>
+__device__ __forceinline__ void fg_stage(const F2 (&acc)[NACC / 2], int i, float* st) {
+    if constexpr (16 * I < NACC) {
+        if (i == I) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                float a, b;
+                split(acc[(16 * I + j) / 2], a, b);
+                st[j * 128] = a;
+                st[(j + 1) * 128] = b;
+            }
+        } else {
+            fg_stage<NACC, I + 1>(acc, i, st);
+        }
+    }
+}
+
 // One tile's outputs.  acc: this thread's weight row (r of the CTA's 128) by ncol X rows from m0; nb:
-// the CTA's first output column; st_off: the warpgroup's staging rows.
-// Staged rows are [128 n] or, gated, [64 gate n | 64 up n with bit 4 flipped] (conflict-free stores).
+// the CTA's first output column; st_off: the warpgroup's staging rows, two buffers of 16, so that the
+// next 16 columns are staged while these are finished.  Staged rows are [128 n] or, gated, [64 gate n |
+// 64 up n with bit 4 flipped] (conflict-free stores).
 template <int ACT, bool GATED, int NACC>
-__device__ __forceinline__ void fg_epilogue(const FgArgs& p, const uint64_t (&acc)[NACC / 2], int ncol, int m0, int nb,
+__device__ __forceinline__ void fg_epilogue(const FgArgs& p, const F2 (&acc)[NACC / 2], int ncol, int m0, int nb,
                                             unsigned char* smem, uint32_t st_off, int r, int bar) {
     // opaque to the compiler: what follows from it is computed here, once a tile, and not kept in
     // registers (or spilled) across the group loop
@@ -166,66 +208,36 @@ __device__ __forceinline__ void fg_epilogue(const FgArgs& p, const uint64_t (&ac
     const int n = nb + n4;
     uint2 bias = make_uint2(0u, 0u);
     if (!GATED && p.bias && n < p.N) bias = *reinterpret_cast<const uint2*>(p.bias + n);
-#pragma unroll
-    for (int c = 0; c < NACC; c += 32) {
-        if (c < ncol) {
-            const int rows = min(min(32, ncol - c), p.M - m0 - c);  // <= 0: nothing of this chunk exists
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                float a, b;
-                unpack_f32x2(acc[(c + i) / 2], a, b);
-                st[i * 128 + col] = a;
-                st[(i + 1) * 128 + col] = b;
-            }
-            wg_barrier(bar);
-            constexpr int RPW = GATED ? 2 : 1;  // rows a warp finishes at once
-            const int row0 = RPW * w + (GATED ? lane >> 4 : 0);
-            int64_t o = (int64_t)(m0 + c + row0) * p.N + n;
-            const float* sr = st + row0 * 128 + n4;
+    constexpr int RPW = GATED ? 2 : 1, RT = 4 / RPW;  // rows a warp finishes at once, rows of a thread
+    const int row0 = RPW * w + (GATED ? lane >> 4 : 0);
+    const int rows = n < p.N ? min(ncol, p.M - m0) : 0;  // of the tile
+    fg_stage<NACC>(acc, 0, st + col);
+    wg_barrier(bar);
 #pragma unroll 1
-            for (int i = 0; i < 8 / RPW; i += 2) {  // two rows' residual loads in flight together
-                const int left = n < p.N ? rows - row0 - 4 * RPW * i : 0;
-                uint2 res[2];
-                if (!GATED && p.residual) {
+    for (int i = 0; 16 * i < ncol; ++i) {
+        const float* sr = st + (i & 1) * 2048 + row0 * 128 + n4;
+        const int left = rows - 16 * i - row0;  // of this thread's rows 0, 4 RPW, ... those below it exist
+        int64_t o = (int64_t)(m0 + 16 * i + row0) * p.N + n;
+        const int64_t step = (int64_t)(4 * RPW) * p.N;
+        if (16 * (i + 1) < ncol) fg_stage<NACC>(acc, i + 1, st + ((i + 1) & 1) * 2048 + col);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (4 * RPW * k < left)
-                            res[k] = *reinterpret_cast<const uint2*>(p.residual + o + (int64_t)(4 * RPW * k) * p.N);
-                }
+        for (int k = 0; k < RT; k += 2) {  // two rows at a time: more do not fit beside the accumulators
+            uint2 res[2];
+            float4 s0[2], s1[2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (4 * RPW * k < left) {
-                        const float4 s0 = *reinterpret_cast<const float4*>(sr + 4 * RPW * k * 128);
-                        float z[4] = {s0.x, s0.y, s0.z, s0.w}, y[4];
-                        if constexpr (GATED) {
-                            const float4 s1 = *reinterpret_cast<const float4*>(sr + 4 * RPW * k * 128 + 64 + (n4 ^ 16) - n4);
-                            const float u[4] = {s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) y[j] = act_fwd<ACT>(z[j]) * u[j];
-                            if (p.U) *reinterpret_cast<uint2*>(p.U + o) = half4(u);
-                        } else {
-                            float f[4];
-                            float4_of(bias, f);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                z[j] += f[j];
-                                y[j] = act_fwd<ACT>(z[j]);
-                            }
-                            if (p.residual) {
-                                float4_of(res[k], f);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) y[j] += f[j];
-                            }
-                        }
-                        *reinterpret_cast<uint2*>(p.Y + o) = half4(y);
-                        if (p.Z) *reinterpret_cast<uint2*>(p.Z + o) = half4(z);
-                    }
-                    o += (int64_t)(4 * RPW) * p.N;
-                }
-                sr += 8 * RPW * 128;
+            for (int j = 0; j < 2; ++j) {
+                if (!GATED && p.residual && 4 * RPW * (k + j) < left)
+                    res[j] = *reinterpret_cast<const uint2*>(p.residual + o + j * step);
+                s0[j] = *reinterpret_cast<const float4*>(sr + 4 * RPW * (k + j) * 128);
+                if (GATED) s1[j] = *reinterpret_cast<const float4*>(sr + 4 * RPW * (k + j) * 128 + 64 + (n4 ^ 16) - n4);
             }
-            wg_barrier(bar);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (4 * RPW * (k + j) < left) fg_finish<ACT, GATED>(p, s0[j], s1[j], bias, res[j], o);
+                o += step;
+            }
         }
+        wg_barrier(bar);
     }
 }
 
@@ -528,14 +540,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             const bool nv = n < p.N;
             const unsigned short* srow = sbase_row + (int64_t)(nv ? n : 0) * p.G;
             uint64_t s4 = nv ? fg_scales4(srow, w.g0, p.G, p.vec) : 0, s4n = 0;
-            uint64_t acc[NACC / 2];
+            F2 acc[NACC / 2];
 #pragma unroll
-            for (int i = 0; i < NACC / 2; ++i) acc[i] = 0;
+            for (int i = 0; i < NACC / 2; ++i) acc[i].v = 0;
             for (int g = w.g0; g < w.g1; ++g) {
                 if ((g & 3) == 0 && g > w.g0) s4 = s4n;
                 if (((g & 3) == 0 || g == w.g0) && nv && (g & ~3) + 4 < p.G) s4n = fg_scales4(srow, (g & ~3) + 4, p.G, p.vec);
                 const float sc = __half2float(__ushort_as_half((unsigned short)(s4 >> (16 * (g & 3)))));
-                const uint64_t sc2 = pack_f32x2(__float_as_uint(sc), __float_as_uint(sc));
+                const F2 sc2 = f2(sc);
                 if (ok && !warp_wait(done_bar(s), ph, abort_flag)) { fail(); ok = false; }
                 if (++s == S) { s = 0; ph ^= 1; }
                 if (ok) {
@@ -560,7 +572,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                                 fg_tie(v[k]);
 #pragma unroll
                                 for (int i = 0; i < 16; i += 2)
-                                    fma2(acc[(c + 16 * k + i) / 2], pack_f32x2(v[k][i], v[k][i + 1]), sc2);
+                                    acc[(c + 16 * k + i) / 2] = fma2(f2(__uint_as_float(v[k][i]), __uint_as_float(v[k][i + 1])), sc2,
+                                                                     acc[(c + 16 * k + i) / 2]);
                             }
                         }
                     }
@@ -574,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
 #pragma unroll
                 for (int c = 0; c < NACC; c += 2) {
                     float v[2];
-                    unpack_f32x2(acc[c / 2], v[0], v[1]);
+                    split(acc[c / 2], v[0], v[1]);
                     if (c < ncol && nv && m0 + c < p.M) P[(int64_t)(m0 + c) * p.N + n] = v[0];
                     if (c < ncol && nv && m0 + c + 1 < p.M) P[(int64_t)(m0 + c + 1) * p.N + n] = v[1];
                 }
@@ -621,8 +634,8 @@ __global__ void __launch_bounds__(256) ffn_reduce_kernel(const float* P, int sli
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[i] += __half2float(bias[n + i]);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = act_fwd<ACT>(z[i]);
+        split(act_fwd2<ACT>(f2(z[0], z[1])), y[0], y[1]);
+        split(act_fwd2<ACT>(f2(z[2], z[3])), y[2], y[3]);
         if constexpr (GATED) {
             const float u[4] = {a[1].x, a[1].y, a[1].z, a[1].w};
 #pragma unroll
