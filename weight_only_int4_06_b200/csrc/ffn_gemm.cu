@@ -19,7 +19,7 @@
 //   warp 0       TMA producer of its CTA: per group X (two boxes of 64 k) and the packed rows
 //   warp 1       CTA 0: issues the pair's tcgen05.mma (M = 256, N = tn, K = 16) and one commit a group
 //   warp 2       TMEM allocation
-//   next 4 DW    dequantise: DW warpgroups take the groups in turn (a row's 128 codes -> 64 TMEM columns)
+//   next 4 DW    dequantise: a thread takes a row's 128 codes of a group
 //   last 8       fold: four take columns 0 .. tn/2 - 1, four the rest: read a group's sums from TMEM,
 //                acc += s * sum in registers; after the last group the epilogue
 // The group sums rotate through NB TMEM buffers, the dequantised groups through AG, so a group's
@@ -56,22 +56,24 @@ constexpr uint32_t FG_EPI = 32 * 128 * 4;          // a fold warpgroup's 32 rows
 
 // NMAX columns at most.
 // 256 (large batches): the dequantised groups lie in shared memory (K-major, 128-byte swizzle).
-// 64 (small batches): in tensor memory, and four warpgroups dequantise, which bounds it.
+// 64 (small batches): in tensor memory; four warpgroups dequantise, and a step is two groups, because a
+// group's products are shorter than the waits, round trips and the issue of a step.
 // Every thread launches with kRegs registers; the fold warps take what the others give up (in
-// warpgroup shares: 24 + 80 + 2 x 200 = 504 of 4 x 128, and 24 + 4 x 64 + 2 x 112 = 504 of 7 x 72).
+// warpgroup shares: 24 + 64 + 2 x 208 = 504 of 4 x 128, and 24 + 4 x 56 + 2 x 128 = 504 of 7 x 72).
 template <int NMAX>
 struct FgCfg {
     static constexpr bool kWide = NMAX > 64;
-    static constexpr int kDW = kWide ? 1 : 4;       // dequantising warpgroups
-    static constexpr int kNB = kWide ? 2 : 4;       // TMEM buffers of group sums
-    static constexpr int kAG = kWide ? 2 : 4;       // dequantised groups
+    static constexpr int kGPS = kWide ? 1 : 2;      // groups per step
+    static constexpr int kDW = kWide ? 1 : 4;       // dequantising warpgroups: kGPS to a step
+    static constexpr int kNB = 2;                   // steps whose sums TMEM holds
+    static constexpr int kAG = 2;                   // dequantised steps
     static constexpr int kThreads = 128 * (1 + kDW + 2);
-    static constexpr uint32_t kACol = kNB * NMAX;   // 64: first TMEM column of the dequantised groups (64 each)
+    static constexpr uint32_t kACol = kNB * kGPS * NMAX;  // 64: first TMEM column of the dequantised groups (64 each)
     static constexpr uint32_t kWBytes = kWide ? 128 * 128 * 2 : 0;  // 256: shared memory of one
     static constexpr int kRegs = kWide ? 128 : 72;
-    static constexpr int kRegsMisc = 24, kRegsDeq = kWide ? 80 : 64, kRegsFold = kWide ? 200 : 112;
+    static constexpr int kRegsMisc = 24, kRegsDeq = kWide ? 64 : 56, kRegsFold = kWide ? 208 : 128;
     static_assert(kRegsMisc + kDW * kRegsDeq + 2 * kRegsFold <= (3 + kDW) * kRegs, "register shares");
-    static_assert(kNB * NMAX + (kWide ? 0 : 64 * kAG) <= 512, "TMEM");
+    static_assert(kNB * kGPS * NMAX + (kWide ? 0 : 64 * kAG * kGPS) <= 512, "TMEM");
 };
 
 struct FgArgs {
@@ -247,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     const __grid_constant__ CUtensorMap tmW1, const FgArgs p) {
     using C = FgCfg<NMAX>;
     constexpr int NACC = NMAX / 2;            // columns per fold thread
-    constexpr int NB = C::kNB, AG = C::kAG, GS = C::kDW;
+    constexpr int NB = C::kNB, AG = C::kAG, GPS = C::kGPS;
     constexpr int FOLD_WARP = 4 + 4 * C::kDW;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_align1024(smem_raw);
@@ -257,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
     const uint32_t rank = cluster_ctarank();
     const int S = p.stages;
     const uint32_t xbytes = (uint32_t)p.tn * 128u;  // tn/2 rows x 128 k x 2 bytes
-    const uint32_t stage_bytes = xbytes + FG_P_BYTES;
+    const uint32_t group_bytes = xbytes + FG_P_BYTES, stage_bytes = GPS * group_bytes;
     const uint32_t w0 = (uint32_t)S * stage_bytes;    // dequantised groups, the epilogue's staging rows, the barriers
     const uint32_t epi0 = w0 + AG * C::kWBytes;
     const uint32_t bar0 = sbase + epi0 + 2 * FG_EPI;
@@ -274,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             mbar_init(full_bar(s), 1);
             mbar_init(done_bar(s), 1);
         }
-        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 8);    // a dequantising warpgroup of each CTA
+        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 8 * GPS);  // a warpgroup of each CTA for each group
         for (int i = 0; i < NB; ++i) mbar_init(d_empty(i), 16);  // eight fold warps of each CTA
         *abort_flag = 0;
         fence_mbarrier_init();
@@ -303,17 +305,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
         regs_dec<C::kRegsMisc>();
         if (warp == 0) {
             // -------------------------------------------------------- TMA producer (one lane issuing)
-            auto load_w = [&](const FgUnit& u, int g, int s) {
-                const uint32_t dst = sbase + (uint32_t)s * stage_bytes + xbytes;
-                if constexpr (GATED) {
-                    const int n = u.nt * 128 + (int)rank * 64;
+            // a step's packed rows
+            auto load_w = [&](const FgUnit& u, int g, int n_groups, int s) {
+                mbar_arrive_expect_tx(full_bar(s), (uint32_t)n_groups * group_bytes);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        tma_load_2d(dst + q * 2048, &tmW0, g * 16, n + 16 * q, full_bar(s));
-                        tma_load_2d(dst + q * 2048 + 1024, &tmW1, g * 16, n + 16 * q, full_bar(s));
+                for (int j = 0; j < GPS; ++j) {
+                    if (j >= n_groups) break;
+                    const uint32_t dst = sbase + (uint32_t)s * stage_bytes + (uint32_t)j * group_bytes + xbytes;
+                    if constexpr (GATED) {
+                        const int n = u.nt * 128 + (int)rank * 64;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            tma_load_2d(dst + q * 2048, &tmW0, (g + j) * 16, n + 16 * q, full_bar(s));
+                            tma_load_2d(dst + q * 2048 + 1024, &tmW1, (g + j) * 16, n + 16 * q, full_bar(s));
+                        }
+                    } else {
+                        tma_load_2d(dst, &tmW0, (g + j) * 16, u.nt * 256 + (int)rank * 128, full_bar(s));
                     }
-                } else {
-                    tma_load_2d(dst, &tmW0, g * 16, u.nt * 256 + (int)rank * 128, full_bar(s));
                 }
             };
             if (!p.early) pdl_wait();
@@ -321,11 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             if (p.early) {  // the first ring's weights, before the preceding kernel has finished
                 for (int u = cluster; u < p.units && ahead < S; u += n_clusters) {
                     const FgUnit w = fg_unit(p, u);
-                    for (int g = w.g0; g < w.g1 && ahead < S; ++g, ++ahead) {
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(full_bar(ahead), stage_bytes);
-                            load_w(w, g, ahead);
-                        }
+                    for (int g = w.g0; g < w.g1 && ahead < S; g += GPS, ++ahead) {
+                        if (elect_one()) load_w(w, g, min(GPS, w.g1 - g), ahead);
                         __syncwarp();
                     }
                 }
@@ -337,16 +342,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
                 const int mx = w.m0 + (int)rank * (p.tn / 2);
-                for (int g = w.g0; g < w.g1; ++g, ++it) {
+                for (int g = w.g0; g < w.g1; g += GPS, ++it) {
                     if (it >= ahead && !mbar_wait_bounded(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
                     if (elect_one()) {
-                        const uint32_t xs = sbase + (uint32_t)s * stage_bytes;
-                        if (it >= ahead) {
-                            mbar_arrive_expect_tx(full_bar(s), stage_bytes);
-                            load_w(w, g, s);
+                        const int n_groups = min(GPS, w.g1 - g);
+                        if (it >= ahead) load_w(w, g, n_groups, s);
+#pragma unroll
+                        for (int j = 0; j < GPS; ++j) {
+                            if (j >= n_groups) break;
+                            const uint32_t xs = sbase + (uint32_t)s * stage_bytes + (uint32_t)j * group_bytes;
+                            tma_load_2d(xs, &tmX, (g + j) * 128, mx, full_bar(s));
+                            tma_load_2d(xs + xbytes / 2, &tmX, (g + j) * 128 + 64, mx, full_bar(s));
                         }
-                        tma_load_2d(xs, &tmX, g * 128, mx, full_bar(s));
-                        tma_load_2d(xs + xbytes / 2, &tmX, g * 128 + 64, mx, full_bar(s));
                     }
                     __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
@@ -366,27 +373,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
-                for (int g = w.g0; g < w.g1; ++g, ++it) {
+                for (int g = w.g0; g < w.g1; g += GPS, ++it) {
                     const int b = it % NB, a = it % AG;
-                    if (!mbar_wait_bounded(d_empty(b), ((uint32_t)(it / NB) & 1) ^ 1, abort_flag) ||
-                        !mbar_wait_bounded(a_full(a), (uint32_t)(it / AG) & 1, abort_flag)) {
+                    // the fold of the step NB ago usually comes last: it is waited for last
+                    if (!mbar_wait_bounded(a_full(a), (uint32_t)(it / AG) & 1, abort_flag) ||
+                        !mbar_wait_bounded(d_empty(b), ((uint32_t)(it / NB) & 1) ^ 1, abort_flag)) {
                         fail();
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes);
-                        const uint64_t ad = sw128_kmajor_desc(sbase + w0 + (uint32_t)a * C::kWBytes);
                         const uint64_t half = (uint64_t)(xbytes / 2) >> 4;  // the second 64 k
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint64_t bj = bd + (j >> 2) * half + 2 * (j & 3);
-                            if constexpr (C::kWide)
-                                mma_f16_ss_pair(tmem + b * NMAX, ad + (j >> 2) * (C::kWBytes / 2 >> 4) + 2 * (j & 3), bj, idesc,
-                                                j != 0);
-                            else
-                                mma_f16_ts_pair(tmem + b * NMAX, tmem + C::kACol + a * 64 + j * 8, bj, idesc, j != 0);
+                        for (int i = 0; i < GPS; ++i) {
+                            if (i > 0 && g + i >= w.g1) break;
+                            const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes + (uint32_t)i * group_bytes);
+                            const uint64_t ad = sw128_kmajor_desc(sbase + w0 + (uint32_t)a * C::kWBytes);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint64_t bj = bd + (j >> 2) * half + 2 * (j & 3);
+                                if constexpr (C::kWide)
+                                    mma_f16_ss_pair(tmem + b * NMAX, ad + (j >> 2) * (C::kWBytes / 2 >> 4) + 2 * (j & 3), bj, idesc,
+                                                    j != 0);
+                                else
+                                    mma_f16_ts_pair(tmem + (b * GPS + i) * NMAX, tmem + C::kACol + (a * GPS + i) * 64 + j * 8, bj,
+                                                    idesc, j != 0);
+                            }
                         }
                         tc_commit_pair(done_bar(s));
                     }
@@ -400,36 +413,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
     } else if (warp < FOLD_WARP) {
         regs_dec<C::kRegsDeq>();
         // ------------------------------------------------------------ dequantisation
-        const int wg = (warp - 4) >> 2, q = warp & 3;  // this warpgroup's groups: wg, wg + GS, ...
+        constexpr int GS = C::kDW / GPS;               // this warpgroup's steps: it, it + GS, ...
+        const int wg = (warp - 4) >> 2, q = warp & 3;
+        const int j = wg % GPS;                        // and its group of them
         const int r = q * 32 + lane;  // row of the CTA's 128 = TMEM lane
         const uint32_t sw = (uint32_t)(r >> 1) & 3;  // 64-byte TMA swizzle
-        const uint32_t c0 = xbytes + (uint32_t)r * 64;
+        const uint32_t c0 = (uint32_t)j * group_bytes + xbytes + (uint32_t)r * 64;
         const uint8_t* zbase = GATED && lane >= 16 ? p.z1 : p.z0;
         const uint32_t remote = map_shared(a_full(0), 0);
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol + (uint32_t)j * 64;
         pdl_wait();  // no bounded wait runs beside the preceding kernel
         bool ok = true;
-        int it = wg, s = wg, sa = wg;  // group, its ring stage, the ring stage of group it - AG (S >= GS, AG)
+        int it = wg / GPS, s = it, sa = it;  // step, its ring stage, the ring stage of step it - AG (S >= GS, AG)
         uint32_t ph = 0, pa = 0;
-        // two of the row's four 16-byte pieces: half h of the group's codes
-        auto load = [&](int h, uint4& wa, uint4& wb) {
-            const unsigned char* st = smem + (uint32_t)s * stage_bytes + c0;
-            wa = *reinterpret_cast<const uint4*>(st + (((2 * h) ^ sw) << 4));
-            wb = *reinterpret_cast<const uint4*>(st + (((2 * h + 1) ^ sw) << 4));
-        };
-        int skip = wg;        // groups of the next unit that are not this warpgroup's
-        bool loaded = false;  // the first half of group it's codes is in wa, wb already
-        uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
+        int skip = it * GPS;  // groups of the next unit before this warpgroup's first step
         for (int u = cluster; u < p.units; u += n_clusters) {
             const FgUnit w = fg_unit(p, u);
             const int n = GATED ? w.nt * 128 + (int)rank * 64 + 16 * q + (lane & 15) : w.nt * 256 + (int)rank * 128 + r;
             const bool nv = n < p.N;
             const uint8_t* zrow = zbase + (int64_t)(nv ? n : 0) * p.G;
-            int g = w.g0 + skip;
-            uint32_t z4 = nv && g < w.g1 ? fg_zeros4(zrow, g, p.G, p.vec) : 0, z4n = 0;
-            int zb = g & ~3;  // z4 holds groups zb ... zb + 3, z4n the next four
+            int gs = w.g0 + skip;  // first group of the step; this warpgroup's is gs + j
+            uint32_t z4 = nv && gs + j < w.g1 ? fg_zeros4(zrow, gs + j, p.G, p.vec) : 0, z4n = 0;
+            int zb = (gs + j) & ~3;  // z4 holds groups zb ... zb + 3, z4n the next four
             if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
-            for (; g < w.g1; g += GS) {
+            for (; gs < w.g1; gs += GS * GPS) {
+                const int g = gs + j;
                 if ((g & ~3) != zb) {  // the next four groups' zero points are fetched while these are used
                     z4 = z4n;
                     zb = g & ~3;
@@ -440,13 +448,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 // high one: exact
                 const uint32_t zl = (0x6400u + z) * 0x10001u, zh = (0xD400u | (z << 4)) * 0x10001u;
                 const uint32_t slot = (uint32_t)(it % AG);
-                // the group that used this slot AG groups ago has been multiplied
-                auto free_slot = [&]() {
-                    if (it >= AG) {
-                        if (ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
-                        sa += GS;
-                        if (sa >= S) { sa -= S; pa ^= 1; }
-                    }
+                // two of the row's four 16-byte pieces: half h of the group's codes
+                auto load = [&](int h, uint32_t (&words)[8]) {
+                    const unsigned char* st = smem + (uint32_t)s * stage_bytes + c0;
+                    const uint4 a = *reinterpret_cast<const uint4*>(st + (((2 * h) ^ sw) << 4));
+                    const uint4 b = *reinterpret_cast<const uint4*>(st + (((2 * h + 1) ^ sw) << 4));
+                    words[0] = a.x; words[1] = a.y; words[2] = a.z; words[3] = a.w;
+                    words[4] = b.x; words[5] = b.y; words[6] = b.z; words[7] = b.w;
                 };
                 auto dequant = [&](uint32_t wd, uint32_t (&o)[4]) {
                     const uint32_t w8 = wd >> 8;
@@ -459,66 +467,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     o[2] = __byte_perm(lo0, hi0, 0x7632);  // k4, k5
                     o[3] = __byte_perm(lo1, hi1, 0x7632);  // k6, k7
                 };
-                if (!loaded) {
-                    if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
-                    load(0, wa, wb);
-                }
-                loaded = false;
-                if constexpr (C::kWide) {
-                    uint4 wc, wd;
-                    load(1, wc, wd);
-                    free_slot();
-                    const uint32_t words[16] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w,
-                                                wc.x, wc.y, wc.z, wc.w, wd.x, wd.y, wd.z, wd.w};
-                    unsigned char* row = smem + w0 + slot * C::kWBytes + (uint32_t)r * 128;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {  // 8-k chunk: block of 64 k, chunk in the row's 128 bytes
-                        uint32_t o[4];
-                        dequant(words[c], o);
-                        *reinterpret_cast<uint4*>(row + (c >> 3) * (C::kWBytes / 2) + (((c & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
+                if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
+                uint32_t words[8];
+                load(0, words);
+                auto free_slot = [&]() {  // the step that used this slot AG steps ago has been multiplied
+                    if (it >= AG) {
+                        if (ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
+                        sa += GS;
+                        if (sa >= S) { sa -= S; pa ^= 1; }
                     }
-                    fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor cores
-                    __syncwarp();
-                    if (ok && lane == 0) mbar_arrive_cluster(remote + 8u * slot);
-                    it += GS;
-                    s += GS;
-                    if (s >= S) { s -= S; ph ^= 1; }
-                } else {
+                };
+                if (C::kWide) free_slot();
+                // past the unit's last group (an odd count's second half): nothing is multiplied
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t words[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (C::kWide) {
+                        unsigned char* row = smem + w0 + slot * C::kWBytes + (uint32_t)h * (C::kWBytes / 2) + (uint32_t)r * 128;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {  // 8-k chunks of the block of 64 k
+                            uint32_t o[4];
+                            dequant(words[c], o);
+                            *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    } else {
                         uint32_t o[32];
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             uint32_t o4[4];
                             dequant(words[c], o4);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) o[4 * c + j] = o4[j];
+                            for (int i = 0; i < 4; ++i) o[4 * c + i] = o4[i];
                         }
                         if (h == 0) {
-                            load(1, wa, wb);
+                            load(1, words);
                             free_slot();
                         }
-                        if (ok) tmem_st_32x32b_x32(taddr + slot * 64 + h * 32, o);
+                        if (ok) tmem_st_32x32b_x32(taddr + slot * (64 * GPS) + h * 32, o);
                     }
-                    it += GS;
-                    s += GS;
-                    if (s >= S) { s -= S; ph ^= 1; }
-                    // the next group's codes, where they have arrived, are read while this one's are stored
-                    if (ok && g + GS < w.g1 && __all_sync(0xffffffffu, mbar_test(full_bar(s), ph))) {
-                        load(0, wa, wb);
-                        loaded = true;
-                    }
-                    if (ok) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(remote + 8u * slot);
-                    }
+                    if (C::kWide && h == 0) load(1, words);
                 }
+                if constexpr (C::kWide) {
+                    fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor cores
+                } else if (ok) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive_cluster(remote + 8u * slot);
+                it += GS;
+                s += GS;
+                if (s >= S) { s -= S; ph ^= 1; }
             }
-            skip = g - w.g1;
+            skip = gs - w.g1;
+            // units end on a step, whole or not: the next unit's first step follows
+            skip = (skip / GPS) * GPS;
         }
     } else {
         regs_inc<C::kRegsFold>();
@@ -540,27 +542,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             const bool nv = n < p.N;
             const unsigned short* srow = sbase_row + (int64_t)(nv ? n : 0) * p.G;
             uint64_t s4 = nv ? fg_scales4(srow, w.g0, p.G, p.vec) : 0, s4n = 0;
+            int sb = w.g0 & ~3;  // s4 holds groups sb ... sb + 3, s4n the next four
+            if (nv && sb + 4 < p.G) s4n = fg_scales4(srow, sb + 4, p.G, p.vec);
             F2 acc[NACC / 2];
 #pragma unroll
             for (int i = 0; i < NACC / 2; ++i) acc[i].v = 0;
-            for (int g = w.g0; g < w.g1; ++g) {
-                if ((g & 3) == 0 && g > w.g0) s4 = s4n;
-                if (((g & 3) == 0 || g == w.g0) && nv && (g & ~3) + 4 < p.G) s4n = fg_scales4(srow, (g & ~3) + 4, p.G, p.vec);
-                const float sc = __half2float(__ushort_as_half((unsigned short)(s4 >> (16 * (g & 3)))));
-                const F2 sc2 = f2(sc);
+            for (int g = w.g0; g < w.g1; g += GPS) {
+                const bool two = GPS == 2 && g + 1 < w.g1;
+                F2 sc[GPS];
+#pragma unroll
+                for (int j = 0; j < GPS; ++j) {
+                    if (((g + j) & ~3) != sb && g + j < w.g1) {
+                        s4 = s4n;
+                        sb += 4;
+                        if (nv && sb + 4 < p.G) s4n = fg_scales4(srow, sb + 4, p.G, p.vec);
+                    }
+                    sc[j] = f2(__half2float(__ushort_as_half((unsigned short)(s4 >> (16 * ((g + j) & 3))))));
+                }
                 if (ok && !warp_wait(done_bar(s), ph, abort_flag)) { fail(); ok = false; }
                 if (++s == S) { s = 0; ph ^= 1; }
                 if (ok) {
                     tc_fence_after();
-                    const uint32_t src = taddr + (uint32_t)(b * NMAX);
-                    // rounds of 32 columns, each one wait (columns past tn hold old sums: never stored)
-                    constexpr int RC = 32;
+                    const uint32_t src = taddr + (uint32_t)(b * GPS * NMAX);
+                    // rounds of 48 columns of one group or 32 of two, each one wait (columns past tn hold old
+                    // sums: never stored)
+                    constexpr int RC = C::kWide ? 48 : 32;
 #pragma unroll
                     for (int c = 0; c < NACC; c += RC) {
                         if (c < ncol) {
-                            uint32_t v[RC / 16][16];
+                            constexpr int KR = RC / 16;
+                            uint32_t v[GPS][KR][16];
 #pragma unroll
-                            for (int k = 0; k < RC / 16; ++k) tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[k]);
+                            for (int k = 0; k < KR; ++k)
+                                if (c + 16 * k < NACC) tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[0][k]);
+                            if (two) {
+#pragma unroll
+                                for (int k = 0; k < KR; ++k) tmem_ld_32x32b_x16(src + (uint32_t)(NMAX + c + 16 * k), v[GPS - 1][k]);
+                            }
                             tmem_wait_ld();
                             if (c + RC >= ncol) {  // all read: the buffer is free
                                 tc_fence_before();
@@ -568,12 +586,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                                 if (lane == 0) mbar_arrive_cluster(remote + 8u * (uint32_t)b);
                             }
 #pragma unroll
-                            for (int k = 0; k < RC / 16; ++k) {
-                                fg_tie(v[k]);
+                            for (int j = 0; j < GPS; ++j) {
+                                if (j == 1 && !two) continue;
 #pragma unroll
-                                for (int i = 0; i < 16; i += 2)
-                                    acc[(c + 16 * k + i) / 2] = fma2(f2(__uint_as_float(v[k][i]), __uint_as_float(v[k][i + 1])), sc2,
-                                                                     acc[(c + 16 * k + i) / 2]);
+                                for (int k = 0; k < KR; ++k) {
+                                    if (c + 16 * k >= NACC) continue;
+                                    fg_tie(v[j][k]);
+#pragma unroll
+                                    for (int i = 0; i < 16; i += 2)
+                                        acc[(c + 16 * k + i) / 2] =
+                                            fma2(f2(__uint_as_float(v[j][k][i]), __uint_as_float(v[j][k][i + 1])), sc[j],
+                                                 acc[(c + 16 * k + i) / 2]);
+                                }
                             }
                         }
                     }
@@ -673,10 +697,10 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
             if (ks > 1 && (tiles * (ks - 1) >= pairs || G / ks < 4)) break;
             const int64_t units = tiles * ks;
             const int64_t waves = (units + pairs - 1) / pairs;
-            // cycles per group: the products (4 tn) or the dequantising warps' issue rate; per unit: filling
-            // and the epilogue; a second launch and its traffic when K is cut
-            const double group = tn > 64 ? std::max(4.6 * tn, 700.0) : 650.0;
-            double t = (double)waves * ((double)((G + ks - 1) / ks) * group + 1500.0 + 8.0 * tn);
+            // cycles per group (measured: 1152 at tn = 192, 1258 at 256, 650 up to 64); per unit: filling and
+            // the epilogue (33 per column); a second launch and its traffic when K is cut
+            const double group = tn > 64 ? 830.0 + 1.67 * tn : 650.0;
+            double t = (double)waves * ((double)((G + ks - 1) / ks) * group + 1500.0 + 33.0 * tn);
             if (ks > 1) t += 4000.0 + (double)ks * (double)M * (double)N * (gated ? 2 : 1) * 8.0 / 3000.0;
             if (best_t < 0.0 || t < best_t) {
                 best_t = t;
@@ -689,7 +713,7 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
         }
     }
     best.wide = best.tn > 64;
-    const uint32_t stage = (uint32_t)best.tn * 128u + FG_P_BYTES;
+    const uint32_t stage = ((uint32_t)best.tn * 128u + FG_P_BYTES) * (uint32_t)(best.wide ? FgCfg<256>::kGPS : FgCfg<64>::kGPS);
     const uint32_t fixed = (best.wide ? FgCfg<256>::kAG * FgCfg<256>::kWBytes : 0) + 2 * FG_EPI + 512;
     best.stages = (int)std::min<uint32_t>((FG_SMEM - 1024 - fixed) / stage, FG_MAXS);
     best.smem = stage * (uint32_t)best.stages + fixed + 1024;
