@@ -588,7 +588,8 @@ w4_status w4_gemm_dx_gated(const uint16_t* dY, int64_t M, int64_t N, int64_t K, 
                            const uint16_t* U, int activation, uint16_t* dG, uint16_t* dU, void* ws,
                            size_t ws_bytes, void* stream);
 
-/* Bytes of device workspace w4_act_backward needs when dbias is wanted (0 is enough otherwise). */
+/* Bytes of device workspace w4_act_backward needs when dbias is wanted (0 is enough otherwise): a
+ * function of M and N (and the device's SM count). */
 w4_status w4_act_backward_workspace_size(int64_t M, int64_t N, size_t* bytes);
 
 /*

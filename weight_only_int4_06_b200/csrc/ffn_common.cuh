@@ -6,9 +6,22 @@
 
 namespace w4 {
 
+// mbar_wait_bounded with long suspended tries (20 us each) and the clock read only after them: two
+// dozen warps wait in turn here, and shorter tries took issue slots from the warps that compute.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
+                                               uint64_t limit_ns = 2000000000ull) {
+    if (mbar_try_wait_suspend(bar, parity, 20000u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait_suspend(bar, parity, 20000u)) return true;
+        if (abort && *abort) return false;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
 // A bounded wait by a whole warp, with one outcome for it (what follows is warp-synchronous).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
+    return __all_sync(0xffffffffu, mbar_wait_long(bar, parity, abort));
 }
 
 // Barrier of one warpgroup.

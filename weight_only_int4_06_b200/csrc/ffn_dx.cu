@@ -168,7 +168,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
             const int my = w.m0 + (int)rank * (p.tn / 2);
             const int kw = (w.k0 + (int)rank * 128) / 8;
             for (int i = w.i0; i < w.i1; ++i, ++it) {
-                if (!mbar_wait_bounded(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
+                if (!mbar_wait_long(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
                 if (elect_one()) {
                     const uint32_t ys = sbase + (uint32_t)s * stage_bytes;
                     const bool second = i >= p.steps1;
@@ -186,8 +186,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
         // Never leave with loads in flight or with the tensor cores still to arrive on this CTA's
         // barriers: wait (bounded) for the last use of every stage.
         for (int i = max(it - S, 0); i < it; ++i) {
-            mbar_wait_bounded(full_bar(i % S), (uint32_t)(i / S) & 1, nullptr, 200000000ull);
-            if (ok) mbar_wait_bounded(done_bar(i % S), (uint32_t)(i / S) & 1, abort_flag);
+            mbar_wait_long(full_bar(i % S), (uint32_t)(i / S) & 1, nullptr, 200000000ull);
+            if (ok) mbar_wait_long(done_bar(i % S), (uint32_t)(i / S) & 1, abort_flag);
         }
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMA issuer (for both CTAs)
@@ -197,10 +197,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
         for (int u = cluster; u < p.units && ok; u += n_clusters, ++ut) {
             const DxUnit w = dx_unit(p, u);
             const int b = ut & 1;
-            if (!mbar_wait_bounded(d_empty(b), ((uint32_t)(ut >> 1) & 1) ^ 1, abort_flag)) { fail(); ok = false; break; }
+            if (!mbar_wait_long(d_empty(b), ((uint32_t)(ut >> 1) & 1) ^ 1, abort_flag)) { fail(); ok = false; break; }
             for (int i = w.i0; i < w.i1; ++i, ++it) {
                 const int a = it % DX_SLOTS;
-                if (!mbar_wait_bounded(a_full(a), (uint32_t)(it / DX_SLOTS) & 1, abort_flag)) { fail(); ok = false; break; }
+                if (!mbar_wait_long(a_full(a), (uint32_t)(it / DX_SLOTS) & 1, abort_flag)) { fail(); ok = false; break; }
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t ad = sw128_mnmajor_desc(sbase + w0 + (uint32_t)a * DX_W_BYTES, DX_W_BYTES / 2);
@@ -218,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
             }
         }
         // on an abort nobody else waits for what was issued: the pair's TMEM is freed after it
-        if (!ok && it > 0) mbar_wait_bounded(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
+        if (!ok && it > 0) mbar_wait_long(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
     } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------ dequantisation
         const int wg = (warp - 4) >> 2;

@@ -56,22 +56,24 @@ constexpr uint32_t FG_EPI = 32 * 128 * 4;          // a fold warpgroup's 32 rows
 
 // NMAX columns at most.
 // 256 (large batches): the dequantised groups lie in shared memory (K-major, 128-byte swizzle).
-// 64 (small batches): in tensor memory; four warpgroups dequantise, and a step is two groups, because a
-// group's products are shorter than the waits, round trips and the issue of a step.
+// 64 (small batches): in tensor memory; a step is two groups, because a group's products are shorter
+// than the waits, round trips and the issue of a step.
 // Every thread launches with kRegs registers; the fold warps take what the others give up (in
-// warpgroup shares: 24 + 64 + 2 x 208 = 504 of 4 x 128, and 24 + 4 x 56 + 2 x 128 = 504 of 7 x 72).
+// warpgroup shares: 24 + 64 + 2 x 208 = 504 of 4 x 128, and 24 + 2 x 80 + 2 x 144 = 472 of 5 x 96).
+// No kernel may spill: with 28 KB of L1 left a reload is an L2 round trip in the group loop.
 template <int NMAX>
 struct FgCfg {
     static constexpr bool kWide = NMAX > 64;
+    static constexpr int kCtas = kWide ? 2 : 1;     // CTAs that share a tile
     static constexpr int kGPS = kWide ? 1 : 2;      // groups per step
-    static constexpr int kDW = kWide ? 1 : 4;       // dequantising warpgroups: kGPS to a step
+    static constexpr int kDW = kGPS;                // dequantising warpgroups: one to each group of a step
     static constexpr int kNB = 2;                   // steps whose sums TMEM holds
     static constexpr int kAG = 2;                   // dequantised steps
     static constexpr int kThreads = 128 * (1 + kDW + 2);
     static constexpr uint32_t kACol = kNB * kGPS * NMAX;  // 64: first TMEM column of the dequantised groups (64 each)
     static constexpr uint32_t kWBytes = kWide ? 128 * 128 * 2 : 0;  // 256: shared memory of one
-    static constexpr int kRegs = kWide ? 128 : 72;
-    static constexpr int kRegsMisc = 24, kRegsDeq = kWide ? 64 : 56, kRegsFold = kWide ? 208 : 128;
+    static constexpr int kRegs = kWide ? 128 : 96;
+    static constexpr int kRegsMisc = 24, kRegsDeq = kWide ? 64 : 80, kRegsFold = kWide ? 208 : 144;
     static_assert(kRegsMisc + kDW * kRegsDeq + 2 * kRegsFold <= (3 + kDW) * kRegs, "register shares");
     static_assert(kNB * kGPS * NMAX + (kWide ? 0 : 64 * kAG * kGPS) <= 512, "TMEM");
 };
@@ -97,6 +99,13 @@ struct FgArgs {
     int early;        // weights may be read before the preceding kernel has finished
     int* status;
 };
+
+// Arrival on the issuing CTA's barrier.
+template <int CTAS>
+__device__ __forceinline__ void fg_arrive(uint32_t bar) {
+    if constexpr (CTAS == 2) mbar_arrive_cluster(bar);
+    else mbar_arrive(bar);
+}
 
 struct FgUnit {
     int m0, nt, slice, g0, g1;
@@ -244,21 +253,24 @@ __device__ __forceinline__ void fg_epilogue(const FgArgs& p, const F2 (&acc)[NAC
 }
 
 template <bool GATED, int NMAX>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThreads, 1)
+__global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
                     const __grid_constant__ CUtensorMap tmW1, const FgArgs p) {
     using C = FgCfg<NMAX>;
     constexpr int NACC = NMAX / 2;            // columns per fold thread
-    constexpr int NB = C::kNB, AG = C::kAG, GPS = C::kGPS;
+    constexpr int NB = C::kNB, AG = C::kAG, GPS = C::kGPS, CTAS = C::kCtas;
+    constexpr int TROWS = 128 * CTAS;         // weight rows of a tile
+    constexpr int TN = GATED ? TROWS / 2 : TROWS;  // outputs n of a tile; TN / CTAS in each CTA
     constexpr int FOLD_WARP = 4 + 4 * C::kDW;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_align1024(smem_raw);
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: the issuing loops stay in uniform registers
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0;
     const int S = p.stages;
-    const uint32_t xbytes = (uint32_t)p.tn * 128u;  // tn/2 rows x 128 k x 2 bytes
+    const int xrows = p.tn / CTAS;                  // X rows in this CTA
+    const uint32_t xbytes = (uint32_t)xrows * 256u;  // 128 k x 2 bytes each
     const uint32_t group_bytes = xbytes + FG_P_BYTES, stage_bytes = GPS * group_bytes;
     const uint32_t w0 = (uint32_t)S * stage_bytes;    // dequantised groups, the epilogue's staging rows, the barriers
     const uint32_t epi0 = w0 + AG * C::kWBytes;
@@ -276,8 +288,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             mbar_init(full_bar(s), 1);
             mbar_init(done_bar(s), 1);
         }
-        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 8 * GPS);  // a warpgroup of each CTA for each group
-        for (int i = 0; i < NB; ++i) mbar_init(d_empty(i), 16);  // eight fold warps of each CTA
+        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 4 * CTAS * GPS);  // a warpgroup of each CTA for each group
+        for (int i = 0; i < NB; ++i) mbar_init(d_empty(i), 8 * CTAS);  // eight fold warps of each CTA
         *abort_flag = 0;
         fence_mbarrier_init();
         prefetch_tmap(&tmX);
@@ -285,12 +297,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
         if (GATED) prefetch_tmap(&tmW1);
     }
     if (warp == 2) {
-        tmem_alloc_pair(smem_u32(tmem_slot), 512);
-        tmem_relinquish_pair();
+        if constexpr (CTAS == 2) {
+            tmem_alloc_pair(smem_u32(tmem_slot), 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), 512);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    if constexpr (CTAS == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     pdl_launch_dependents();
@@ -299,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
         *abort_flag = 1;
         record_status(p.status, W4_ERR_DEVICE_TIMEOUT);
     };
-    const int cluster = (int)blockIdx.x >> 1, n_clusters = (int)gridDim.x >> 1;
+    const int cluster = (int)blockIdx.x / CTAS, n_clusters = (int)gridDim.x / CTAS;
 
     if (warp < 4) {
         regs_dec<C::kRegsMisc>();
@@ -313,14 +330,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     if (j >= n_groups) break;
                     const uint32_t dst = sbase + (uint32_t)s * stage_bytes + (uint32_t)j * group_bytes + xbytes;
                     if constexpr (GATED) {
-                        const int n = u.nt * 128 + (int)rank * 64;
+                        const int n = u.nt * TN + (int)rank * 64;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             tma_load_2d(dst + q * 2048, &tmW0, (g + j) * 16, n + 16 * q, full_bar(s));
                             tma_load_2d(dst + q * 2048 + 1024, &tmW1, (g + j) * 16, n + 16 * q, full_bar(s));
                         }
                     } else {
-                        tma_load_2d(dst, &tmW0, (g + j) * 16, u.nt * 256 + (int)rank * 128, full_bar(s));
+                        tma_load_2d(dst, &tmW0, (g + j) * 16, u.nt * TN + (int)rank * 128, full_bar(s));
                     }
                 }
             };
@@ -341,9 +358,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
                 const FgUnit w = fg_unit(p, u);
-                const int mx = w.m0 + (int)rank * (p.tn / 2);
+                const int mx = w.m0 + (int)rank * xrows;
                 for (int g = w.g0; g < w.g1; g += GPS, ++it) {
-                    if (it >= ahead && !mbar_wait_bounded(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
+                    if (it >= ahead && !mbar_wait_long(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
                     if (elect_one()) {
                         const int n_groups = min(GPS, w.g1 - g);
                         if (it >= ahead) load_w(w, g, n_groups, s);
@@ -362,12 +379,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
             // Never leave with loads in flight or with the tensor cores still to arrive on this CTA's
             // barriers: wait (bounded) for the last use of every stage.
             for (int i = max(it - S, 0); i < it; ++i) {
-                mbar_wait_bounded(full_bar(i % S), (uint32_t)(i / S) & 1, nullptr, 200000000ull);
-                if (ok) mbar_wait_bounded(done_bar(i % S), (uint32_t)(i / S) & 1, abort_flag);
+                mbar_wait_long(full_bar(i % S), (uint32_t)(i / S) & 1, nullptr, 200000000ull);
+                if (ok) mbar_wait_long(done_bar(i % S), (uint32_t)(i / S) & 1, abort_flag);
             }
         } else if (warp == 1 && rank == 0) {
             // -------------------------------------------------------- MMA issuer (for both CTAs)
-            const uint32_t idesc = idesc_f16_f32(256, p.tn);
+            const uint32_t idesc = idesc_f16_f32(TROWS, p.tn);
             pdl_wait();
             int it = 0, s = 0;
             bool ok = true;
@@ -376,8 +393,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 for (int g = w.g0; g < w.g1; g += GPS, ++it) {
                     const int b = it % NB, a = it % AG;
                     // the fold of the step NB ago usually comes last: it is waited for last
-                    if (!mbar_wait_bounded(a_full(a), (uint32_t)(it / AG) & 1, abort_flag) ||
-                        !mbar_wait_bounded(d_empty(b), ((uint32_t)(it / NB) & 1) ^ 1, abort_flag)) {
+                    if (!mbar_wait_long(a_full(a), (uint32_t)(it / AG) & 1, abort_flag) ||
+                        !mbar_wait_long(d_empty(b), ((uint32_t)(it / NB) & 1) ^ 1, abort_flag)) {
                         fail();
                         ok = false;
                         break;
@@ -397,47 +414,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                                     mma_f16_ss_pair(tmem + b * NMAX, ad + (j >> 2) * (C::kWBytes / 2 >> 4) + 2 * (j & 3), bj, idesc,
                                                     j != 0);
                                 else
-                                    mma_f16_ts_pair(tmem + (b * GPS + i) * NMAX, tmem + C::kACol + (a * GPS + i) * 64 + j * 8, bj,
-                                                    idesc, j != 0);
+                                    mma_f16_ts(tmem + (b * GPS + i) * NMAX, tmem + C::kACol + (a * GPS + i) * 64 + j * 8, bj, idesc,
+                                               j != 0);
                             }
                         }
-                        tc_commit_pair(done_bar(s));
+                        if constexpr (CTAS == 2) tc_commit_pair(done_bar(s));
+                        else tc_commit(done_bar(s));
                     }
                     __syncwarp();
                     if (++s == S) s = 0;
                 }
             }
             // on an abort nobody else waits for what was issued: the pair's TMEM is freed after it
-            if (!ok && it > 0) mbar_wait_bounded(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
+            if (!ok && it > 0) mbar_wait_long(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
         }
     } else if (warp < FOLD_WARP) {
         regs_dec<C::kRegsDeq>();
         // ------------------------------------------------------------ dequantisation
-        constexpr int GS = C::kDW / GPS;               // this warpgroup's steps: it, it + GS, ...
         const int wg = (warp - 4) >> 2, q = warp & 3;
-        const int j = wg % GPS;                        // and its group of them
+        const int j = wg;  // its group of every step
         const int r = q * 32 + lane;  // row of the CTA's 128 = TMEM lane
         const uint32_t sw = (uint32_t)(r >> 1) & 3;  // 64-byte TMA swizzle
         const uint32_t c0 = (uint32_t)j * group_bytes + xbytes + (uint32_t)r * 64;
         const uint8_t* zbase = GATED && lane >= 16 ? p.z1 : p.z0;
-        const uint32_t remote = map_shared(a_full(0), 0);
+        const uint32_t remote = CTAS == 2 ? map_shared(a_full(0), 0) : a_full(0);
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol + (uint32_t)j * 64;
         pdl_wait();  // no bounded wait runs beside the preceding kernel
         bool ok = true;
-        int it = wg / GPS, s = it, sa = it;  // step, its ring stage, the ring stage of step it - AG (S >= GS, AG)
+        int it = 0, s = 0, sa = 0;  // step, its ring stage, the ring stage of step it - AG (S >= AG)
         uint32_t ph = 0, pa = 0;
-        int skip = it * GPS;  // groups of the next unit before this warpgroup's first step
         for (int u = cluster; u < p.units; u += n_clusters) {
             const FgUnit w = fg_unit(p, u);
-            const int n = GATED ? w.nt * 128 + (int)rank * 64 + 16 * q + (lane & 15) : w.nt * 256 + (int)rank * 128 + r;
+            const int n = w.nt * TN + (GATED ? (int)rank * 64 + 16 * q + (lane & 15) : (int)rank * 128 + r);
             const bool nv = n < p.N;
             const uint8_t* zrow = zbase + (int64_t)(nv ? n : 0) * p.G;
-            int gs = w.g0 + skip;  // first group of the step; this warpgroup's is gs + j
-            uint32_t z4 = nv && gs + j < w.g1 ? fg_zeros4(zrow, gs + j, p.G, p.vec) : 0, z4n = 0;
-            int zb = (gs + j) & ~3;  // z4 holds groups zb ... zb + 3, z4n the next four
+            uint32_t z4 = nv && w.g0 + j < w.g1 ? fg_zeros4(zrow, w.g0 + j, p.G, p.vec) : 0, z4n = 0;
+            int zb = (w.g0 + j) & ~3;  // z4 holds groups zb ... zb + 3, z4n the next four
             if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
-            for (; gs < w.g1; gs += GS * GPS) {
-                const int g = gs + j;
+            for (int gs = w.g0; gs < w.g1; gs += GPS, ++it) {
+                const int g = gs + j;  // past the last group of an odd count: dequantised all the same, not multiplied
                 if ((g & ~3) != zb) {  // the next four groups' zero points are fetched while these are used
                     z4 = z4n;
                     zb = g & ~3;
@@ -470,15 +485,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                 if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
                 uint32_t words[8];
                 load(0, words);
+                uint32_t next[8];
+                if (C::kWide) load(1, next);
                 auto free_slot = [&]() {  // the step that used this slot AG steps ago has been multiplied
                     if (it >= AG) {
                         if (ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
-                        sa += GS;
-                        if (sa >= S) { sa -= S; pa ^= 1; }
+                        if (++sa == S) { sa = 0; pa ^= 1; }
                     }
                 };
                 if (C::kWide) free_slot();
-                // past the unit's last group (an odd count's second half): nothing is multiplied
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if constexpr (C::kWide) {
@@ -504,7 +519,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                         }
                         if (ok) tmem_st_32x32b_x32(taddr + slot * (64 * GPS) + h * 32, o);
                     }
-                    if (C::kWide && h == 0) load(1, words);
+                    if (C::kWide && h == 0) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) words[c] = next[c];
+                    }
                 }
                 if constexpr (C::kWide) {
                     fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor cores
@@ -513,14 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive_cluster(remote + 8u * slot);
-                it += GS;
-                s += GS;
-                if (s >= S) { s -= S; ph ^= 1; }
+                if (ok && lane == 0) fg_arrive<CTAS>(remote + 8u * slot);
+                if (++s == S) { s = 0; ph ^= 1; }
             }
-            skip = gs - w.g1;
-            // units end on a step, whole or not: the next unit's first step follows
-            skip = (skip / GPS) * GPS;
         }
     } else {
         regs_inc<C::kRegsFold>();
@@ -530,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
         const int ncol = p.tn / 2;
         const bool upper = lane >= 16;
         const unsigned short* sbase_row = GATED && upper ? p.s1 : p.s0;
-        const uint32_t remote = map_shared(d_empty(0), 0);
+        const uint32_t remote = CTAS == 2 ? map_shared(d_empty(0), 0) : d_empty(0);
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(f * ncol);
         pdl_wait();  // the outputs may be read, the residual written, by the preceding kernel
         bool ok = true;
@@ -538,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
         uint32_t ph = 0;
         for (int u = cluster; u < p.units; u += n_clusters) {
             const FgUnit w = fg_unit(p, u);
-            const int n = GATED ? w.nt * 128 + (int)rank * 64 + 16 * q + (lane & 15) : w.nt * 256 + (int)rank * 128 + r;
+            const int n = w.nt * TN + (GATED ? (int)rank * 64 + 16 * q + (lane & 15) : (int)rank * 128 + r);
             const bool nv = n < p.N;
             const unsigned short* srow = sbase_row + (int64_t)(nv ? n : 0) * p.G;
             uint64_t s4 = nv ? fg_scales4(srow, w.g0, p.G, p.vec) : 0, s4n = 0;
@@ -583,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                             if (c + RC >= ncol) {  // all read: the buffer is free
                                 tc_fence_before();
                                 __syncwarp();
-                                if (lane == 0) mbar_arrive_cluster(remote + 8u * (uint32_t)b);
+                                if (lane == 0) fg_arrive<CTAS>(remote + 8u * (uint32_t)b);
                             }
 #pragma unroll
                             for (int j = 0; j < GPS; ++j) {
@@ -616,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
                     if (c < ncol && nv && m0 + c + 1 < p.M) P[(int64_t)(m0 + c + 1) * p.N + n] = v[1];
                 }
             } else {
-                const int nb = GATED ? w.nt * 128 + (int)rank * 64 : w.nt * 256 + (int)rank * 128;
+                const int nb = w.nt * TN + (int)rank * (TN / CTAS);
                 dispatch_act(p.act, [&](auto act) {
                     fg_epilogue<decltype(act)::value, GATED, NACC>(p, acc, ncol, m0, nb, smem, epi0 + (uint32_t)f * FG_EPI, r, 1 + f);
                     return cudaSuccess;
@@ -625,10 +638,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FgCfg<NMAX>::kThread
         }
     }
     __syncthreads();
-    cluster_sync();  // nothing of the pair's products or arrivals is outstanding in either CTA
+    if constexpr (CTAS == 2) cluster_sync();  // nothing of the pair's products or arrivals is outstanding in either CTA
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 512);
+        if constexpr (CTAS == 2) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
     }
 }
 
@@ -684,22 +698,23 @@ struct FgPlan {
 };
 
 FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
-    const int64_t pairs = std::max(1, device_sm_count() / 2), G = K / 128;
-    const int64_t rows = gated ? 128 : 256;
-    const int64_t n_tiles = (N + rows - 1) / rows;
+    const int64_t sms = std::max(2, device_sm_count()), G = K / 128;
     FgPlan best = {};
     double best_t = -1.0;
     for (int tn = 32; tn <= 256; tn += 32) {
         if (tn > 32 && tn >= M + 32) break;
-        const int64_t m_tiles = (M + tn - 1) / tn;
+        const bool wide = tn > 64;
+        const int64_t slots = wide ? sms / 2 : sms;  // tiles at a time
+        const int64_t rows = (wide ? 256 : 128) / (gated ? 2 : 1);
+        const int64_t m_tiles = (M + tn - 1) / tn, n_tiles = (N + rows - 1) / rows;
         const int64_t tiles = m_tiles * n_tiles;
         for (int ks = 1; ks <= 16 && ks <= G; ++ks) {
-            if (ks > 1 && (tiles * (ks - 1) >= pairs || G / ks < 4)) break;
+            if (ks > 1 && (tiles * (ks - 1) >= slots || G / ks < 4)) break;
             const int64_t units = tiles * ks;
-            const int64_t waves = (units + pairs - 1) / pairs;
-            // cycles per group (measured: 1152 at tn = 192, 1258 at 256, 650 up to 64); per unit: filling and
+            const int64_t waves = (units + slots - 1) / slots;
+            // cycles per group (measured: 1152 at tn = 192, 1258 at 256, 500 up to 64); per unit: filling and
             // the epilogue (33 per column); a second launch and its traffic when K is cut
-            const double group = tn > 64 ? 830.0 + 1.67 * tn : 650.0;
+            const double group = wide ? 830.0 + 1.67 * tn : 500.0;
             double t = (double)waves * ((double)((G + ks - 1) / ks) * group + 1500.0 + 33.0 * tn);
             if (ks > 1) t += 4000.0 + (double)ks * (double)M * (double)N * (gated ? 2 : 1) * 8.0 / 3000.0;
             if (best_t < 0.0 || t < best_t) {
@@ -713,7 +728,8 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
         }
     }
     best.wide = best.tn > 64;
-    const uint32_t stage = ((uint32_t)best.tn * 128u + FG_P_BYTES) * (uint32_t)(best.wide ? FgCfg<256>::kGPS : FgCfg<64>::kGPS);
+    const uint32_t group = (uint32_t)best.tn * (best.wide ? 128u : 256u) + FG_P_BYTES;
+    const uint32_t stage = group * (uint32_t)(best.wide ? FgCfg<256>::kGPS : FgCfg<64>::kGPS);
     const uint32_t fixed = (best.wide ? FgCfg<256>::kAG * FgCfg<256>::kWBytes : 0) + 2 * FG_EPI + 512;
     best.stages = (int)std::min<uint32_t>((FG_SMEM - 1024 - fixed) / stage, FG_MAXS);
     best.smem = stage * (uint32_t)best.stages + fixed + 1024;
@@ -744,7 +760,8 @@ cudaError_t fg_launch(const CUtensorMap& tx, const CUtensorMap& t0, const CUtens
     const cudaError_t e = fg_setup<GATED, NMAX>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * std::min(pl.units, std::max(1, device_sm_count() / 2))), 1, 1);
+    constexpr int ctas = FgCfg<NMAX>::kCtas;
+    cfg.gridDim = dim3((unsigned)(ctas * std::min(pl.units, std::max(1, device_sm_count() / ctas))), 1, 1);
     cfg.blockDim = dim3(FgCfg<NMAX>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
@@ -793,7 +810,7 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
     if (pl.ks > 1 && !ws) return cudaErrorInvalidValue;
     CUtensorMap tx, t0, t1;
     if (!make_tensor_map_2d(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)K, (uint64_t)M, 64,
-                            (uint32_t)(pl.tn / 2),
+                            (uint32_t)(pl.wide ? pl.tn / 2 : pl.tn),
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     const uint32_t box = gated ? 16 : 128;
