@@ -3,7 +3,8 @@
     python -m weight_only_int4_06_b200.build_lib [--verbose-ptxas]
 
 Objects go to weight_only_int4_06_b200/_build/ (git-ignored); the shared library is written next
-to this file so that it travels with the source tree.  Rebuilds only what changed.
+to this file so that it travels with the source tree, and so is _ffn_call.so, the compiled half of the
+Python binding (built with g++ against torch's headers).  Rebuilds only what changed.
 """
 from __future__ import annotations
 
@@ -21,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libw4a16.so")
+CALL_SRC = os.path.join(CSRC, "ffn_call.cpp")
+CALL = os.path.join(PKG, "_ffn_call.so")  # importable as weight_only_int4_06_b200._ffn_call
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -80,12 +83,37 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     return LIB
 
 
+def build_call(force: bool = False) -> str:
+    """The compiled half of the Python binding (host code against torch's headers)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    deps = max(os.path.getmtime(CALL_SRC), os.path.getmtime(os.path.join(INCLUDE, "w4a16.h")))
+    if not force and os.path.exists(CALL) and os.path.getmtime(CALL) >= deps:
+        return CALL
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    tmp = CALL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, *[a for d in inc for a in ("-isystem", d)], CALL_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda",
+           "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("building _ffn_call.so failed")
+    os.replace(tmp, CALL)
+    return CALL
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--verbose-ptxas", action="store_true")
     ap.add_argument("--force", action="store_true")
     a = ap.parse_args()
     print(build(a.verbose_ptxas, a.force))
+    print(build_call(a.force))
 
 
 if __name__ == "__main__":

@@ -667,6 +667,34 @@ def _current_stream(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+# The usual case of the five calls below, compiled (csrc/ffn_call.cpp): the same checks, allocations and
+# C call.  It hands back whatever is not the usual case, which the Python here then takes.
+_FAST_ENTRIES = ("w4_gemm_fused", "w4_gemm_gated", "w4_gemm_dx", "w4_gemm_dx_gated", "w4_act_backward",
+                 "w4_gemm_fused_workspace_size", "w4_gemm_gated_workspace_size", "w4_gemm_dx_workspace_size",
+                 "w4_act_backward_workspace_size")
+_fast_module = None
+
+
+def _fast():
+    global _fast_module
+    if _fast_module is None:
+        L = lib()
+        try:
+            from weight_only_int4_06_b200 import _ffn_call
+        except ImportError as e:
+            raise RuntimeError("_ffn_call.so not built; run `python -m weight_only_int4_06_b200.build_lib`") from e
+        _ffn_call.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _FAST_ENTRIES))
+        _fast_module = _ffn_call
+    return _fast_module
+
+
+def _done(r, where: str):
+    """A compiled call's outcome: its outputs, or the error its status stands for."""
+    if r.__class__ is int:
+        raise W4Error(r, where)
+    return r
+
+
 _ffn_ws_cache: dict = {}
 
 
@@ -719,6 +747,11 @@ def w4_gemm_fused(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, z
                   stream=None):
     """Y = act(X . dequant(W)^T + bias) + residual; with save_pre (Y, Z), Z = X . dequant(W)^T + bias.
     `out` may be the residual (added in place)."""
+    if stream is None:
+        r = (_fast_module or _fast()).fused(X, packed, scales, zeros, bias, activation, residual, save_pre, group, out,
+                                            workspace, flags)
+        if r is not NotImplemented:
+            return _done(r, "w4_gemm_fused")
     M, K = _matrix(X, "X")
     N = _matrix(packed, "packed")[0]
     dev = _on_gpu(X, "X")
@@ -750,6 +783,10 @@ def w4_gemm_gated(X: torch.Tensor, gate, up, activation: int = ACT_SILU, save_pr
                   stream=None):
     """H = act(X . Wg^T) * (X . Wu^T); gate and up: (packed, scales, zeros) each.  With save_pre
     (H, G, U), the two projections that the backward pass takes."""
+    if stream is None:
+        r = (_fast_module or _fast()).gated(X, gate, up, activation, save_pre, group, out, workspace, flags)
+        if r is not NotImplemented:
+            return _done(r, "w4_gemm_gated")
     M, K = _matrix(X, "X")
     N = _matrix(gate[0], "gate packed")[0]
     dev = _on_gpu(X, "X")
@@ -779,6 +816,10 @@ def w4_gemm_dx(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
                dY2: torch.Tensor | None = None, weights2=None, group: int = 128, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dX = dY . dequant(W) (+ dY2 . dequant(W2), weights2 = (packed, scales, zeros)), [M, K]."""
+    if stream is None:
+        r = (_fast_module or _fast()).dx(dY, packed, scales, zeros, dY2, weights2, group, out, workspace)
+        if r is not NotImplemented:
+            return _done(r, "w4_gemm_dx")
     M, N = _matrix(dY, "dY")
     K = _matrix(packed, "packed")[1] * 8
     dev = _on_gpu(dY, "dY")
@@ -806,6 +847,11 @@ def w4_gemm_dx_gated(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
                      workspace: torch.Tensor | None = None, stream=None):
     """(dG, dU) [M, K] from dH = dY . dequant(W): dG = dH U act'(G), dU = dH act(G).  out = (dG, dU)
     may be (G, U) (in place)."""
+    if stream is None:
+        out0, out1 = out if out is not None else (None, None)
+        r = (_fast_module or _fast()).dx_gated(dY, packed, scales, zeros, G, U, activation, group, out0, out1, workspace)
+        if r is not NotImplemented:
+            return _done(r, "w4_gemm_dx_gated")
     M, N = _matrix(dY, "dY")
     K = _matrix(packed, "packed")[1] * 8
     dev = _on_gpu(dY, "dY")
@@ -837,6 +883,11 @@ def w4_act_backward(dY: torch.Tensor, Z: torch.Tensor | None, U: torch.Tensor | 
     """The activation's backward pass.  Without U: dZ = dY act'(Z), and with bias_grad (dZ, dbias), dbias [N]
     fp32 the column sums of dZ.  With U (gated: Z is G): (dG, dU) = (dY U act'(Z), dY act(Z)).
     out: dZ, or (dG, dU), possibly the inputs' own buffers.  With ACT_NONE and no U, Z may be None."""
+    if stream is None:
+        out0, out1 = (out, None) if U is None else (out if out is not None else (None, None))
+        r = (_fast_module or _fast()).act_backward(dY, Z, U, activation, bias_grad, out0, out1, workspace)
+        if r is not NotImplemented:
+            return _done(r, "w4_act_backward")
     M, N = _matrix(dY, "dY")
     dev = _on_gpu(dY, "dY")
     other = _other_context(dev, stream)
