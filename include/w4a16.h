@@ -529,6 +529,10 @@ w4_status w4_gemm_fused_workspace_size(int64_t M, int64_t N, int64_t K, int grou
  *   place); Y [M, N] fp16 out; Z [M, N] fp16 out or NULL: X . W^T + bias, which w4_act_backward
  *   takes.
  *   flags: 0 or W4_FLAG_WEIGHTS_STATIC (see w4_variant; covers packed, scales and zeros).
+ *   M <= 8 goes through w4_gemm's GEMV where one launch serves the shape and scales and zeros are
+ *   16-byte aligned; it stages half of the activations as fp16(x / 16), which moves an |x| below
+ *   2^-10 by up to 2^-21.  Everything else is summed exactly as stored: per group of 128 the products
+ *   x (q - z) in fp32 on the tensor cores, times s in fp32.
  *   Backward pass: w4_act_backward (dZ, dbias; skip it without activation and bias), w4_gemm_dx;
  *   the residual's gradient is dY.
  * Errors: W4_ERR_UNSUPPORTED for an unknown activation or flag; else as w4_gemm.
@@ -566,7 +570,9 @@ w4_status w4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int n_layer
  * or of two layers of the same shape that share their input (gate and up projection).
  *
  *   dY, dY2 [M, N] fp16; W, W2 [N, K] (quantised along K as everywhere); dX [M, K] fp16 out.  One
- *   layer: dY2, packed2, scales2 and zeros2 all NULL; two layers: none of them.
+ *   layer: dY2, packed2, scales2 and zeros2 all NULL; two layers: none of them.  The contraction runs
+ *   across the groups' scales, so each weight (q - z) s is rounded once to fp16 before the
+ *   fp32-accumulating tensor-core product.
  * Errors: as w4_gemm; W4_ERR_NULL when the second layer is given in part.
  */
 w4_status w4_gemm_dx(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
@@ -576,7 +582,7 @@ w4_status w4_gemm_dx(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const 
 
 /*
  * w4_gemm_dx_gated -- the down projection's input gradient carried through the gate, without
- * storing it: dH = dY . W [M, K] (fp32), then
+ * storing it: dH = dY . W [M, K] (as w4_gemm_dx forms it, kept in fp32), then
  *     dG = dH * U * act'(G),  dU = dH * act(G).
  *
  *   dY [M, N] fp16; W [N, K] the down projection (K the gated block's inner size); G, U [M, K] fp16

@@ -224,6 +224,23 @@ def test_act_backward_identity():
     assert torch.allclose(db.double(), dY.double().sum(0), atol=1e-4)
 
 
+def test_bias_gradient_without_dz():
+    """The C call with W4_ACT_NONE: no Z, no dZ, the bias gradient alone."""
+    import ctypes
+    M, N = 300, 520
+    dY = dev(normal(2, M, N, 1.0))
+    db = torch.empty(N, dtype=torch.float32, device="cuda")
+    need = B.w4_act_backward_workspace_size(M, N)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    P = lambda t: ctypes.c_void_p(t.data_ptr())
+    st = B.lib().w4_act_backward(P(dY), None, None, M, N, B.ACT_NONE, None, None, P(db), P(ws), need,
+                                 ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0
+    ref = dY.double().sum(0)
+    # fp32 sums of M terms
+    assert bool(((db.double() - ref).abs() <= M * 2.0 ** -24 * dY.double().abs().sum(0)).all())
+
+
 def test_activation_extremes():
     """Saved pre-activations at the ends of fp16, infinite ones and NaN: finite inputs give finite
     gradients, infinities the limits, NaN stays NaN."""
@@ -450,6 +467,70 @@ def test_block_trains_and_serves_captured(M):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(eager, out))
     compare(out)
+    ok()
+
+
+def test_concurrent_streams():
+    """Calls that overlap on two streams, each with its own workspace, do not disturb each other."""
+    M, N, K = 40, 1024, 4096
+    w = [dlayer(layer(90 + i, N, K)) for i in range(2)]
+    X = [dev(synth.layer_case(90 + i, M, K, 8)[0]) for i in range(2)]
+    dY = [dev(normal([14, i], M, N, 0.05)) for i in range(2)]
+
+    def step(i):
+        return (B.w4_gemm_fused(X[i], *w[i], activation=B.ACT_SILU), B.w4_gemm_gated(X[i], w[i], w[1 - i]),
+                B.w4_gemm_dx(dY[i], *w[i], dY2=dY[i], weights2=w[1 - i]))
+
+    want = [step(0), step(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+    ok()
+
+
+def test_compiled_and_plain_binding_agree():
+    """The binding's compiled usual case and its Python (taken with an explicit stream, parameters or a
+    list of weights) give the same results and refuse the same arguments."""
+    M, N, K = 5, 264, 512
+    X = dev(synth.layer_case(92, M, K, 8)[0])
+    a, b = dlayer(layer(92, N, K)), dlayer(layer(93, N, K))
+    dY, G = dev(normal(15, M, N, 0.05)), dev(normal(16, M, K, 1.0))
+    here = torch.cuda.current_stream()
+    calls = [
+        lambda **k: B.w4_gemm_fused(X, *a, bias=dY[0].contiguous(), activation=B.ACT_RELU, residual=dY, save_pre=True, **k),
+        lambda **k: B.w4_gemm_gated(X, a, b, save_pre=True, **k),
+        lambda **k: (B.w4_gemm_dx(dY, *a, dY2=dY, weights2=b, **k),),
+        lambda **k: B.w4_gemm_dx_gated(dY, *a, G, G, **k),
+        lambda **k: B.w4_act_backward(dY, dY, bias_grad=True, **k),
+        lambda **k: B.w4_act_backward(dY, dY, U=dY, **k),
+    ]
+    for f in calls:
+        assert all(torch.equal(x, y) for x, y in zip(f(), f(stream=here)))
+    assert torch.equal(B.w4_gemm_gated(X, a, b), B.w4_gemm_gated(torch.nn.Parameter(X), list(a), b))
+    for bad in (lambda: B.w4_gemm_fused(X, *a, bias=dY), lambda: B.w4_gemm_fused(X[:, ::2], *a),
+                lambda: B.w4_gemm_fused(X, *a, residual=G), lambda: B.w4_gemm_fused(X, *a, out=G),
+                lambda: B.w4_gemm_gated(X, a, (b[0], b[1], b[2].cpu())), lambda: B.w4_gemm_dx(dY, *a, dY2=dY),
+                lambda: B.w4_gemm_dx_gated(dY, *a, G, G[:, :256]), lambda: B.w4_act_backward(dY, G),
+                lambda: B.w4_gemm_fused(X, *a, workspace=torch.empty(4))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: B.w4_gemm_fused(X.float(), *a), lambda: B.w4_gemm_fused(X, a[0], a[1].float(), a[2]),
+                lambda: B.w4_act_backward(dY, dY.float())):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: B.w4_gemm_fused(X, *a, activation=9), lambda: B.w4_gemm_fused(X, *a, flags=3),
+                lambda: B.w4_act_backward(dY, dY, U=dY, bias_grad=True),
+                lambda: B.w4_act_backward(dY, None, activation=B.ACT_SILU)):
+        with pytest.raises(B.W4Error):
+            bad()
     ok()
 
 

@@ -20,8 +20,9 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, vo
 }
 
 // A bounded wait by a whole warp, with one outcome for it (what follows is warp-synchronous).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait_long(bar, parity, abort));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns = 2000000000ull) {
+    return __all_sync(0xffffffffu, mbar_wait_long(bar, parity, abort, limit_ns));
 }
 
 // Barrier of one warpgroup.

@@ -309,7 +309,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
         for (int u = cluster; u < p.units; u += n_clusters, ++ut) {
             const DxUnit w = dx_unit(p, u);
             const int b = ut & 1;
-            if (ok && !warp_wait(d_full(b), (uint32_t)(ut >> 1) & 1, abort_flag)) { fail(); ok = false; }
+            // a whole tile's products: the limit grows with its steps (under 1 us each)
+            const uint64_t limit = 2000000000ull + 10000ull * (uint64_t)(w.i1 - w.i0);
+            if (ok && !warp_wait(d_full(b), (uint32_t)(ut >> 1) & 1, abort_flag, limit)) { fail(); ok = false; }
             if (wg_barrier_any(1 + f, !ok)) { ok = false; continue; }  // all four warps agree before the staging barriers
             tc_fence_after();
             const int m0 = w.m0 + f * ncol, kb = w.k0 + (int)rank * 128, k = kb + 4 * lane;

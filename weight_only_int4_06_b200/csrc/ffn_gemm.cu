@@ -59,7 +59,7 @@ constexpr uint32_t FG_EPI = 32 * 128 * 4;          // a fold warpgroup's 32 rows
 // 64 (small batches): in tensor memory; a step is two groups, because a group's products are shorter
 // than the waits, round trips and the issue of a step.
 // Every thread launches with kRegs registers; the fold warps take what the others give up (in
-// warpgroup shares: 24 + 64 + 2 x 208 = 504 of 4 x 128, and 24 + 2 x 80 + 2 x 144 = 472 of 5 x 96).
+// warpgroup shares: 24 + 80 + 2 x 200 = 504 of 4 x 128, and 24 + 2 x 80 + 2 x 144 = 472 of 5 x 96).
 // No kernel may spill: with 28 KB of L1 left a reload is an L2 round trip in the group loop.
 template <int NMAX>
 struct FgCfg {
@@ -73,7 +73,7 @@ struct FgCfg {
     static constexpr uint32_t kACol = kNB * kGPS * NMAX;  // 64: first TMEM column of the dequantised groups (64 each)
     static constexpr uint32_t kWBytes = kWide ? 128 * 128 * 2 : 0;  // 256: shared memory of one
     static constexpr int kRegs = kWide ? 128 : 96;
-    static constexpr int kRegsMisc = 24, kRegsDeq = kWide ? 64 : 80, kRegsFold = kWide ? 208 : 144;
+    static constexpr int kRegsMisc = 24, kRegsDeq = 80, kRegsFold = kWide ? 200 : 144;
     static_assert(kRegsMisc + kDW * kRegsDeq + 2 * kRegsFold <= (3 + kDW) * kRegs, "register shares");
     static_assert(kNB * kGPS * NMAX + (kWide ? 0 : 64 * kAG * kGPS) <= 512, "TMEM");
 };
@@ -577,9 +577,9 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                 if (ok) {
                     tc_fence_after();
                     const uint32_t src = taddr + (uint32_t)(b * GPS * NMAX);
-                    // rounds of 48 columns of one group or 32 of two, each one wait (columns past tn hold old
-                    // sums: never stored)
-                    constexpr int RC = C::kWide ? 48 : 32;
+                    // rounds of 32 columns (of both groups), each one wait; columns past tn hold old sums: never
+                    // stored.  Longer rounds take registers that the dequantising warps use better (48: 3 % slower)
+                    constexpr int RC = 32;
 #pragma unroll
                     for (int c = 0; c < NACC; c += RC) {
                         if (c < ncol) {
@@ -587,7 +587,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                             uint32_t v[GPS][KR][16];
 #pragma unroll
                             for (int k = 0; k < KR; ++k)
-                                if (c + 16 * k < NACC) tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[0][k]);
+                                tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[0][k]);
                             if (two) {
 #pragma unroll
                                 for (int k = 0; k < KR; ++k) tmem_ld_32x32b_x16(src + (uint32_t)(NMAX + c + 16 * k), v[GPS - 1][k]);
@@ -603,7 +603,6 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                                 if (j == 1 && !two) continue;
 #pragma unroll
                                 for (int k = 0; k < KR; ++k) {
-                                    if (c + 16 * k >= NACC) continue;
                                     fg_tie(v[j][k]);
 #pragma unroll
                                     for (int i = 0; i < 16; i += 2)
