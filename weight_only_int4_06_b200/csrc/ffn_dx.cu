@@ -275,11 +275,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
                         hi0 = hmul2_u32(hi0, s2);
                         lo1 = hmul2_u32(lo1, s2);
                         hi1 = hmul2_u32(hi1, s2);
-                        uint4 o;
-                        o.x = __byte_perm(lo0, hi0, 0x5410);
-                        o.y = __byte_perm(lo1, hi1, 0x5410);
-                        o.z = __byte_perm(lo0, hi0, 0x7632);
-                        o.w = __byte_perm(lo1, hi1, 0x7632);
+                        // the pairs as they come: eight k are stored in the order 0 4 1 5 2 6 3 7, which orders the
+                        // product's rows; the epilogue puts them back
+                        const uint4 o = make_uint4(lo0, hi0, lo1, hi1);
                         const uint32_t ch = (uint32_t)(4 * c + j);  // 8-k chunk 0 .. 15: block of 64 k, chunk in it
                         *reinterpret_cast<uint4*>(smem + wrow + (ch >> 3) * (DX_W_BYTES / 2) +
                                                   (((ch & 7) ^ ((uint32_t)r & 7)) << 4)) = o;
@@ -304,6 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
         const uint32_t remote = map_shared(d_empty(0), 0);
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(f * ncol);
         float* st = reinterpret_cast<float*>(smem + epi0 + (uint32_t)f * DX_EPI);
+        const int kr = (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2);  // the k of this lane's row of the product
         bool ok = true;
         int ut = 0;
         for (int u = cluster; u < p.units; u += n_clusters, ++ut) {
@@ -328,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
                 }
                 const int rows = min(min(32, ncol - c), p.M - m0 - c);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) st[i * 128 + r] = __uint_as_float(v[i]);
+                for (int i = 0; i < 32; ++i) st[i * 128 + kr] = __uint_as_float(v[i]);
                 wg_barrier(1 + f);
                 int64_t o = (int64_t)(m0 + c + q) * p.K + k;
                 const float* sr = st + q * 128 + 4 * lane;

@@ -57,7 +57,8 @@ constexpr uint32_t FG_EPI = 32 * 128 * 4;          // a fold warpgroup's 32 rows
 // NMAX columns at most.
 // 256 (large batches): the dequantised groups lie in shared memory (K-major, 128-byte swizzle).
 // 64 (small batches): in tensor memory; a step is two groups, because a group's products are shorter
-// than the waits, round trips and the issue of a step.
+// than the waits, round trips and the issue of a step, and because TMA moves a 128-byte row in the
+// time of a 64-byte one.
 // Every thread launches with kRegs registers; the fold warps take what the others give up (in
 // warpgroup shares: 24 + 80 + 2 x 200 = 504 of 4 x 128, and 24 + 2 x 80 + 2 x 144 = 472 of 5 x 96).
 // No kernel may spill: with 28 KB of L1 left a reload is an L2 round trip in the group loop.
@@ -271,7 +272,8 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
     const int S = p.stages;
     const int xrows = p.tn / CTAS;                  // X rows in this CTA
     const uint32_t xbytes = (uint32_t)xrows * 256u;  // 128 k x 2 bytes each
-    const uint32_t group_bytes = xbytes + FG_P_BYTES, stage_bytes = GPS * group_bytes;
+    // a stage: X of the step's groups, then their packed codes, rows of 64 GPS bytes
+    const uint32_t p_off = GPS * xbytes, stage_bytes = GPS * (xbytes + FG_P_BYTES);
     const uint32_t w0 = (uint32_t)S * stage_bytes;    // dequantised groups, the epilogue's staging rows, the barriers
     const uint32_t epi0 = w0 + AG * C::kWBytes;
     const uint32_t bar0 = sbase + epi0 + 2 * FG_EPI;
@@ -322,23 +324,19 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
         regs_dec<C::kRegsMisc>();
         if (warp == 0) {
             // -------------------------------------------------------- TMA producer (one lane issuing)
-            // a step's packed rows
+            // a step's packed rows (all GPS groups' bytes: past the last group of an odd count too)
             auto load_w = [&](const FgUnit& u, int g, int n_groups, int s) {
-                mbar_arrive_expect_tx(full_bar(s), (uint32_t)n_groups * group_bytes);
+                mbar_arrive_expect_tx(full_bar(s), (uint32_t)n_groups * xbytes + GPS * FG_P_BYTES);
+                const uint32_t dst = sbase + (uint32_t)s * stage_bytes + p_off;
+                if constexpr (GATED) {
+                    const int n = u.nt * TN + (int)rank * 64;
 #pragma unroll
-                for (int j = 0; j < GPS; ++j) {
-                    if (j >= n_groups) break;
-                    const uint32_t dst = sbase + (uint32_t)s * stage_bytes + (uint32_t)j * group_bytes + xbytes;
-                    if constexpr (GATED) {
-                        const int n = u.nt * TN + (int)rank * 64;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tma_load_2d(dst + q * 2048, &tmW0, (g + j) * 16, n + 16 * q, full_bar(s));
-                            tma_load_2d(dst + q * 2048 + 1024, &tmW1, (g + j) * 16, n + 16 * q, full_bar(s));
-                        }
-                    } else {
-                        tma_load_2d(dst, &tmW0, (g + j) * 16, u.nt * TN + (int)rank * 128, full_bar(s));
+                    for (int q = 0; q < 4; ++q) {
+                        tma_load_2d(dst + q * (2048 * GPS), &tmW0, g * 16, n + 16 * q, full_bar(s));
+                        tma_load_2d(dst + q * (2048 * GPS) + 1024 * GPS, &tmW1, g * 16, n + 16 * q, full_bar(s));
                     }
+                } else {
+                    tma_load_2d(dst, &tmW0, g * 16, u.nt * TN + (int)rank * 128, full_bar(s));
                 }
             };
             if (!p.early) pdl_wait();
@@ -367,7 +365,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
 #pragma unroll
                         for (int j = 0; j < GPS; ++j) {
                             if (j >= n_groups) break;
-                            const uint32_t xs = sbase + (uint32_t)s * stage_bytes + (uint32_t)j * group_bytes;
+                            const uint32_t xs = sbase + (uint32_t)s * stage_bytes + (uint32_t)j * xbytes;
                             tma_load_2d(xs, &tmX, (g + j) * 128, mx, full_bar(s));
                             tma_load_2d(xs + xbytes / 2, &tmX, (g + j) * 128 + 64, mx, full_bar(s));
                         }
@@ -405,7 +403,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
 #pragma unroll
                         for (int i = 0; i < GPS; ++i) {
                             if (i > 0 && g + i >= w.g1) break;
-                            const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes + (uint32_t)i * group_bytes);
+                            const uint64_t bd = sw128_kmajor_desc(sbase + (uint32_t)s * stage_bytes + (uint32_t)i * xbytes);
                             const uint64_t ad = sw128_kmajor_desc(sbase + w0 + (uint32_t)a * C::kWBytes);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
@@ -434,8 +432,9 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
         const int wg = (warp - 4) >> 2, q = warp & 3;
         const int j = wg;  // its group of every step
         const int r = q * 32 + lane;  // row of the CTA's 128 = TMEM lane
-        const uint32_t sw = (uint32_t)(r >> 1) & 3;  // 64-byte TMA swizzle
-        const uint32_t c0 = (uint32_t)j * group_bytes + xbytes + (uint32_t)r * 64;
+        // TMA swizzle of the row's 16-byte pieces: 64-byte rows by bits 1-2 of the row, 128-byte ones by 0-2
+        const uint32_t sw = GPS == 1 ? (uint32_t)(r >> 1) & 3 : (uint32_t)r & 7;
+        const uint32_t c0 = p_off + (uint32_t)r * (64 * GPS);
         const uint8_t* zbase = GATED && lane >= 16 ? p.z1 : p.z0;
         const uint32_t remote = CTAS == 2 ? map_shared(a_full(0), 0) : a_full(0);
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol + (uint32_t)j * 64;
@@ -466,8 +465,8 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                 // two of the row's four 16-byte pieces: half h of the group's codes
                 auto load = [&](int h, uint32_t (&words)[8]) {
                     const unsigned char* st = smem + (uint32_t)s * stage_bytes + c0;
-                    const uint4 a = *reinterpret_cast<const uint4*>(st + (((2 * h) ^ sw) << 4));
-                    const uint4 b = *reinterpret_cast<const uint4*>(st + (((2 * h + 1) ^ sw) << 4));
+                    const uint4 a = *reinterpret_cast<const uint4*>(st + (((4 * j + 2 * h) ^ sw) << 4));
+                    const uint4 b = *reinterpret_cast<const uint4*>(st + (((4 * j + 2 * h + 1) ^ sw) << 4));
                     words[0] = a.x; words[1] = a.y; words[2] = a.z; words[3] = a.w;
                     words[4] = b.x; words[5] = b.y; words[6] = b.z; words[7] = b.w;
                 };
@@ -812,14 +811,15 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
                             (uint32_t)(pl.wide ? pl.tn / 2 : pl.tn),
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    const uint32_t box = gated ? 16 : 128;
-    if (!make_tensor_map_2d(&t0, w.packed, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, (uint64_t)(K / 8), (uint64_t)N, 16, box,
-                            CU_TENSOR_MAP_SWIZZLE_64B))
-        return cudaErrorInvalidValue;
+    // packed rows in pieces of a step's groups: 64 bytes each
+    auto packed_map = [&](CUtensorMap* t, const uint32_t* packed) {
+        return make_tensor_map_2d(t, packed, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, (uint64_t)(K / 8), (uint64_t)N,
+                                  16u * (uint32_t)(pl.wide ? FgCfg<256>::kGPS : FgCfg<64>::kGPS), gated ? 16 : 128,
+                                  pl.wide ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (!packed_map(&t0, w.packed)) return cudaErrorInvalidValue;
     t1 = t0;
-    if (gated && !make_tensor_map_2d(&t1, w2->packed, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, (uint64_t)(K / 8), (uint64_t)N, 16,
-                                     box, CU_TENSOR_MAP_SWIZZLE_64B))
-        return cudaErrorInvalidValue;
+    if (gated && !packed_map(&t1, w2->packed)) return cudaErrorInvalidValue;
     const int64_t G = K / 128;
     auto vec_ok = [&](const W4Layer& l) {  // 4-group vectors at multiples of 4 groups of every row
         return G % 4 == 0 && (reinterpret_cast<uintptr_t>(l.scales) & 7) == 0 && (reinterpret_cast<uintptr_t>(l.zeros) & 3) == 0;
