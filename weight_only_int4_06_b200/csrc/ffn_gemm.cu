@@ -458,9 +458,10 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                     if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
                 }
                 const uint32_t z = (z4 >> (8 * (g & 3))) & 0xFFu;
-                // q - z = (1024 + q) - (1024 + z) from a low nibble, (1024 + 16 q) / 16 - (64 + z) from a
-                // high one: exact
-                const uint32_t zl = (0x6400u + z) * 0x10001u, zh = (0xD400u | (z << 4)) * 0x10001u;
+                // A byte in both halves of a word, the low nibble kept in the lower and the high one in the
+                // upper, under the exponent of 1024: the pair 1024 + q, 1024 + 16 q'.  Then (1024 + q) * 1 - (1024
+                // + z) and (1024 + 16 q') / 16 - (64 + z): q - z and q' - z, exact.  Three instructions a pair.
+                const uint32_t zadd = (0xE400u + z) | ((0xD400u | (z << 4)) << 16);
                 const uint32_t slot = (uint32_t)(it % AG);
                 // two of the row's four 16-byte pieces: half h of the group's codes
                 auto load = [&](int h, uint32_t (&words)[8]) {
@@ -471,15 +472,10 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                     words[4] = b.x; words[5] = b.y; words[6] = b.z; words[7] = b.w;
                 };
                 auto dequant = [&](uint32_t wd, uint32_t (&o)[4]) {
-                    const uint32_t w8 = wd >> 8;
-                    const uint32_t lo0 = hsub2_u32(lop3_and_or(wd, 0x000F000Fu, 0x64006400u), zl);              // k0, k4
-                    const uint32_t hi0 = hfma2_u32(lop3_and_or(wd, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k1, k5
-                    const uint32_t lo1 = hsub2_u32(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), zl);              // k2, k6
-                    const uint32_t hi1 = hfma2_u32(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh);  // k3, k7
-                    o[0] = __byte_perm(lo0, hi0, 0x5410);  // k0, k1
-                    o[1] = __byte_perm(lo1, hi1, 0x5410);  // k2, k3
-                    o[2] = __byte_perm(lo0, hi0, 0x7632);  // k4, k5
-                    o[3] = __byte_perm(lo1, hi1, 0x7632);  // k6, k7
+                    o[0] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x0000), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
+                    o[1] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x1111), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
+                    o[2] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x2222), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
+                    o[3] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x3333), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
                 };
                 if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
                 uint32_t words[8];
@@ -586,10 +582,11 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                             uint32_t v[GPS][KR][16];
 #pragma unroll
                             for (int k = 0; k < KR; ++k)
-                                tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[0][k]);
+                                if (C::kWide || c + 16 * k < ncol) tmem_ld_32x32b_x16(src + (uint32_t)(c + 16 * k), v[0][k]);
                             if (two) {
 #pragma unroll
-                                for (int k = 0; k < KR; ++k) tmem_ld_32x32b_x16(src + (uint32_t)(NMAX + c + 16 * k), v[GPS - 1][k]);
+                                for (int k = 0; k < KR; ++k)
+                                    if (c + 16 * k < ncol) tmem_ld_32x32b_x16(src + (uint32_t)(NMAX + c + 16 * k), v[GPS - 1][k]);
                             }
                             tmem_wait_ld();
                             if (c + RC >= ncol) {  // all read: the buffer is free
@@ -602,6 +599,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                                 if (j == 1 && !two) continue;
 #pragma unroll
                                 for (int k = 0; k < KR; ++k) {
+                                    if (!C::kWide && c + 16 * k >= ncol) continue;
                                     fg_tie(v[j][k]);
 #pragma unroll
                                     for (int i = 0; i < 16; i += 2)

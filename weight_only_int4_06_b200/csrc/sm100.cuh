@@ -279,16 +279,8 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 }
 
 // Both CTAs' tensor cores on one product, issued by one thread of CTA 0: D [256, n], rows 0-127 in
-// CTA 0's TMEM and 128-255 in CTA 1's; A likewise (TMEM or shared memory), B's rows halved over the
-// two CTAs' shared memory at the same offset.
-__device__ __forceinline__ void mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
+// CTA 0's TMEM and 128-255 in CTA 1's; A's rows likewise and B's rows halved over the two CTAs' shared
+// memory, at the same offsets.
 __device__ __forceinline__ void mma_f16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                 uint32_t accumulate) {
     asm volatile(
