@@ -45,6 +45,8 @@ template <int ACT, bool GATED, bool SUM>
 __global__ void __launch_bounds__(AB_THREADS, AB_SUM_CTAS) act_backward_kernel(const uint4* dY, const uint4* Z, const uint4* U,
                                                                   int64_t M, int64_t N8, int64_t rows, int cw, uint4* dZ,
                                                                   uint4* dU, float* part) {
+    pdl_launch_dependents();
+    pdl_wait();
     constexpr int AB_ROWS = SUM ? 4 : 2;  // rows a thread loads together
     const int rl = AB_THREADS / cw, lane = threadIdx.x / cw;
     const int64_t c = (int64_t)blockIdx.x * cw + threadIdx.x % cw;
@@ -155,22 +157,8 @@ cudaError_t launch_act_backward(const uint16_t* dY, const uint16_t* Z, const uin
     float* part = dbias ? static_cast<float*>(ws) : nullptr;
     auto p = [](const uint16_t* q) { return reinterpret_cast<const uint4*>(q); };
     auto o = [](uint16_t* q) { return reinterpret_cast<uint4*>(q); };
-    cudaError_t e = dispatch_act(activation, [&](auto act) {
-        constexpr int ACT = decltype(act)::value;
-        if (U)
-            act_backward_kernel<ACT, true, false>
-                <<<grid, AB_THREADS, 0, stream>>>(p(dY), p(Z), p(U), M, N8, pl.rows, pl.cw, o(dZ), o(dU), nullptr);
-        else if (dbias)
-            act_backward_kernel<ACT, false, true>
-                <<<grid, AB_THREADS, 0, stream>>>(p(dY), p(Z), nullptr, M, N8, pl.rows, pl.cw, o(dZ), nullptr, part);
-        else
-            act_backward_kernel<ACT, false, false>
-                <<<grid, AB_THREADS, 0, stream>>>(p(dY), p(Z), nullptr, M, N8, pl.rows, pl.cw, o(dZ), nullptr, nullptr);
-        return cudaGetLastError();
-    });
-    if (e != cudaSuccess || !dbias) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((N + 31) / 32), 1, 1);
+    cudaLaunchConfig_t cfg = {};  // both launches: programmatic dependents of what precedes them
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(AB_THREADS, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -178,6 +166,20 @@ cudaError_t launch_act_backward(const uint16_t* dY, const uint16_t* Z, const uin
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    const uint4* none = nullptr;
+    cudaError_t e = dispatch_act(activation, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        if (U)
+            return cudaLaunchKernelEx(&cfg, act_backward_kernel<ACT, true, false>, p(dY), p(Z), p(U), M, N8, pl.rows, pl.cw,
+                                      o(dZ), o(dU), part);
+        if (dbias)
+            return cudaLaunchKernelEx(&cfg, act_backward_kernel<ACT, false, true>, p(dY), p(Z), none, M, N8, pl.rows, pl.cw,
+                                      o(dZ), o(nullptr), part);
+        return cudaLaunchKernelEx(&cfg, act_backward_kernel<ACT, false, false>, p(dY), p(Z), none, M, N8, pl.rows, pl.cw,
+                                  o(dZ), o(nullptr), part);
+    });
+    if (e != cudaSuccess || !dbias) return e;
+    cfg.gridDim = dim3((unsigned)((N + 31) / 32), 1, 1);
     return cudaLaunchKernelEx(&cfg, column_sum_kernel, (const float*)part, pl.blocks, N, dbias);
 }
 

@@ -758,7 +758,8 @@ static cudaError_t ds_launch(const CUtensorMap& tm, const CUtensorMap& tmS, cons
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = weights_static ? 1 : 0;
+    // with an epilogue always: without static weights every warp waits for the preceding kernel first
+    cfg.numAttrs = weights_static || EPI != 0 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, decode_stream_kernel<MT, SG, KS, EPI>, tm, tmS, tmZ,
                               reinterpret_cast<const __half*>(X), reinterpret_cast<const unsigned short*>(scales),
                               zeros, reinterpret_cast<__half*>(Y), P, (int)M, (int)N, (int)K, p.n_tiles, p.ns, p.nms,

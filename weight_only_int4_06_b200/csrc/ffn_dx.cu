@@ -160,6 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer (one lane issuing)
+        pdl_wait();  // every role: nothing is read, written or timed beside the preceding kernel
         int it = 0, s = 0;
         uint32_t ph = 1;
         bool ok = true;
@@ -192,6 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMA issuer (for both CTAs)
         const uint32_t idesc = idesc_f16_f32(256, p.tn) | kIdescAMnMajor;
+        pdl_wait();
         int it = 0, s = 0, ut = 0;
         bool ok = true;
         for (int u = cluster; u < p.units && ok; u += n_clusters, ++ut) {
@@ -227,6 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
         const uint32_t wrow = w0 + (uint32_t)wg * DX_W_BYTES + (uint32_t)r * 128;  // DX_SLOTS == 2: a slot each
         const uint32_t remote = map_shared(a_full(wg), 0);
         const int64_t G = p.K >> 7;
+        pdl_wait();
         bool ok = true;
         int it = wg, s = wg, sa = wg;  // step, its ring stage, the ring stage of step it - 2
         uint32_t ph = 0, pa = 0;
@@ -302,6 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
         const uint32_t remote = map_shared(d_empty(0), 0);
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(f * ncol);
         float* st = reinterpret_cast<float*>(smem + epi0 + (uint32_t)f * DX_EPI);
+        pdl_wait();
         const int kr = (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2);  // the k of this lane's row of the product
         bool ok = true;
         int ut = 0;
@@ -371,7 +375,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
-    pdl_wait();
 }
 
 // The slices' partial sums [slice][M][K] in slice order, then the outputs.  A programmatic dependent
@@ -501,20 +504,23 @@ cudaError_t launch_ffn_dx(const uint16_t* dY, const W4Layer& w, const uint16_t* 
     a.stages = pl.stages;
     a.status = status;
     const int clusters = std::min(pl.units, std::max(1, device_sm_count() / 2));
-    ffn_dx_kernel<<<2 * clusters, DX_THREADS, pl.smem, stream>>>(ty[0], ty[1], tw[0], tw[1], a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || pl.ks == 1) return e;
-    const int64_t mk = M * K;
-    const int64_t want = (mk / 4 + 255) / 256, cap = (int64_t)device_sm_count() * 8;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min(want, cap), 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
+    cudaLaunchConfig_t cfg = {};  // both launches: programmatic dependents of what precedes them
+    cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+    cfg.blockDim = dim3(DX_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, ffn_dx_kernel, ty[0], ty[1], tw[0], tw[1], a);
+    if (e != cudaSuccess || pl.ks == 1) return e;
+    const int64_t mk = M * K;
+    const int64_t want = (mk / 4 + 255) / 256, cap = (int64_t)device_sm_count() * 8;
+    cfg.gridDim = dim3((unsigned)std::min(want, cap), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.dynamicSmemBytes = 0;
     return dispatch_gate(gate != nullptr, a.act, [&](auto act) {
         return cudaLaunchKernelEx(&cfg, dx_reduce_kernel<decltype(act)::value>, (const float*)a.P, pl.ks, mk, a.G, a.U, a.out,
                                   a.out2);

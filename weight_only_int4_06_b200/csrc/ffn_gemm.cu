@@ -761,11 +761,13 @@ cudaError_t fg_launch(const CUtensorMap& tx, const CUtensorMap& t0, const CUtens
     cfg.blockDim = dim3(FgCfg<NMAX>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
+    // A programmatic dependent of whatever precedes it: set-up overlaps the predecessor's end; every
+    // role waits for that end before it touches global memory (but for static weights, `early`)
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = args.early ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<GATED, NMAX>, tx, t0, t1, args);
 }
 
