@@ -577,3 +577,58 @@ def test_gradients_against_differences(M):
     # G, U, dG and dU rounded to fp16: a few half steps of the gradient's rms, as a 2-norm
     err = (dX - diff)[:, ::5]
     assert np.linalg.norm(err) <= 4 * HALF * np.linalg.norm(diff[:, ::5])
+
+
+@pytest.mark.parametrize("M", [1, 6, 40, 300])
+def test_launches_wait_for_whatever_precedes_them(M):
+    """Each call directly behind the work that makes its inputs -- the quantisation of its weights, a copy,
+    a memset, a long kernel, another stream's joined work -- eagerly and captured: the bits of calls with a
+    synchronisation before each."""
+    N, K = 512, 1024
+    W0, W1 = (dev(normal([17, i], N, K, 0.03)) for i in range(2))
+    X0, dY0, G0 = dev(normal(18, M, K, 1.0)), dev(normal(19, M, N, 0.05)), dev(normal(20, M, K, 1.0))
+    long = dev(normal(21, 2048, 2048, 0.01))
+    side = torch.cuda.Stream()
+
+    def step(between):
+        out = []
+        layers = []
+        for W in (W0, W1):
+            Wc = W.clone()
+            between()
+            layers.append(B.w4_quantize_pack(Wc))
+        X, dY, G = torch.empty_like(X0), torch.empty_like(dY0), torch.zeros_like(G0)
+        between()
+        out.append(B.w4_gemm_fused(X.copy_(X0), *layers[0], activation=B.ACT_SILU))  # behind a copy
+        between()
+        out.append(B.w4_gemm_gated(X.zero_(), *layers, save_pre=True)[1])  # behind a memset
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.mm(long, long)
+            dY.copy_(dY0)
+        torch.mm(long, long)
+        here.wait_stream(side)  # two predecessors
+        between()
+        out.append(B.w4_gemm_dx(dY, *layers[0], dY2=dY, weights2=layers[1]))
+        between()
+        out.append(B.w4_gemm_dx_gated(dY, *layers[0], G.copy_(G0), G)[0])
+        between()
+        out += B.w4_act_backward(out[0], out[0], bias_grad=True)
+        between()
+        out.append(B.w4_gemm_fused(X.copy_(X0), *layers[1], residual=out[0], out=torch.empty_like(out[0])))
+        return out
+
+    want = step(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, step(lambda: None)))
+    graph, main = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=main):
+        got = step(lambda: None)
+    for _ in range(3):
+        for t in got:
+            t.fill_(7.0)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    ok()

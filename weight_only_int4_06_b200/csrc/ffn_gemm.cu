@@ -7,29 +7,34 @@
 // (a weight (q - z) s rounded to fp16 costs 1.5e-4 of the result in 2-norm, as much again as the
 // output's own rounding; in the gated product it enters twice).
 //
-// One cluster of two CTAs computes a tile of 256 weight rows by `tn` (32 ... NMAX) rows of X. The
-// weights are the A operand, written by the dequantising threads straight into tensor memory (thread
-// = weight row = TMEM lane); X is the B operand, half of its rows in each CTA's shared memory.  Why
-// this way round: the weights never pass through shared memory as fp16, which a 256 x 192 tile's
-// shared-memory port could not carry beside the tensor cores' own reads (per group of 128 and CTA:
-// X in 24 KB, X out 24 KB, codes in and out 16 KB, 64 KB in the 768 cycles of its products; weights
-// as fp16 would add 64 KB); a thread owns one weight row, so a group has one scale per thread; and
-// small batches cost products of 32 columns, not 128.
+// The weights are the A operand (256 or 128 rows), dequantised once per tile; X is the B operand (`tn`
+// rows).  Why this way round: a thread owns one weight row, so a group has one scale per thread, and small
+// batches cost products of 32 columns, not 128.  Two instantiations:
+//   NMAX 256  large batches: two CTAs share a tile of 256 weight rows by up to 256 rows of X, each with half
+//             of both in its shared memory (cta_group::2).  The weights go through shared memory as fp16:
+//             144 KB a group and CTA pass its port (X in and out 64, codes in and out 16, weights in and
+//             out 64) beside 1024 cycles of products, so port and tensor cores are about equally busy.
+//             Weights in tensor memory would spare the port 64 KB but leave columns for 192 rows of X only,
+//             whose group took 1152 cycles where 256 take 1258: slower by a fifth.
+//   NMAX 64   small batches: one CTA, 128 weight rows by up to 64 rows of X, the weights in tensor memory,
+//             two groups a step.  Bound by instruction issue, half of it the dequantisation's: 57 us at
+//             M = 32, K = 28672, N = 8192, where HBM would allow 19.
+// At M = 2048, K = 4096, N = 11008: gated 291 us (1270 TFLOP/s), plain 150 us.
 //
-//   warp 0       TMA producer of its CTA: per group X (two boxes of 64 k) and the packed rows
-//   warp 1       CTA 0: issues the pair's tcgen05.mma (M = 256, N = tn, K = 16) and one commit a group
+//   warp 0       TMA producer of its CTA: X (boxes of 64 k) and the packed rows of a step
+//   warp 1       first CTA: issues the tcgen05.mma (N = tn, K = 16) and one commit a step
 //   warp 2       TMEM allocation
 //   next 4 DW    dequantise: a thread takes a row's 128 codes of a group
 //   last 8       fold: four take columns 0 .. tn/2 - 1, four the rest: read a group's sums from TMEM,
 //                acc += s * sum in registers; after the last group the epilogue
-// The group sums rotate through NB TMEM buffers, the dequantised groups through AG, so a group's
-// products, the next ones' dequantisation and the last one's fold overlap.  One barrier per ring
+// The group sums rotate through NB TMEM buffers, the dequantised steps through AG, so a step's
+// products, the next one's dequantisation and the last one's fold overlap.  One barrier per ring
 // stage (committed once by the tensor cores) tells the producer that the stage, the dequantising warps
-// that the group's TMEM columns are free, and the fold warps that the sums are there.
+// that the dequantised step is free, and the fold warps that the sums are there.
 //
-// Epilogue: the fold warps pass 32 columns at a time through shared memory as fp32 [m][n], so that the
-// output, residual and pre-activation rows are read and written as whole 256-byte rows (from the
-// accumulators' own layout, thread = n, a warp's stores were 64-byte pieces: 25 cycles each).
+// Epilogue: the fold warps pass 16 columns at a time through shared memory as fp32 [m][n], two buffers of
+// them, so that the output, residual and pre-activation rows are read and written as whole 256-byte rows
+// (from the accumulators' own layout, thread = n, a warp's stores were 64-byte pieces: 25 cycles each).
 // Gated: the 32 lanes of a warp hold 16 gate rows and the 16 up rows of the same n, so both factors of
 // an output lie in one CTA's rows.
 //
@@ -423,7 +428,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                     if (++s == S) s = 0;
                 }
             }
-            // on an abort nobody else waits for what was issued: the pair's TMEM is freed after it
+            // on an abort nobody else waits for what was issued: the TMEM is freed after it
             if (!ok && it > 0) mbar_wait_long(done_bar((it - 1) % S), (uint32_t)((it - 1) / S) & 1, nullptr, 200000000ull);
         }
     } else if (warp < FOLD_WARP) {
@@ -708,9 +713,12 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
             if (ks > 1 && (tiles * (ks - 1) >= slots || G / ks < 4)) break;
             const int64_t units = tiles * ks;
             const int64_t waves = (units + slots - 1) / slots;
-            // cycles per group (measured: 1152 at tn = 192, 1258 at 256, 500 up to 64); per unit: filling and
-            // the epilogue (33 per column); a second launch and its traffic when K is cut
-            const double group = wide ? 830.0 + 1.67 * tn : 500.0;
+            // cycles per group (measured: 1152 at tn = 192, 1258 at 256); per unit: filling and the epilogue (33
+            // per column); a second launch and its traffic when K is cut.  Small tiles: 880 a group measured
+            // with every SM at work, less with some idle; 700 chooses best between the two instantiations.
+            // 500 leaves M = 128, K = 28672, N = 8192 to small tiles (128 us, 100 in large ones) and the gated
+            // M = 256, K = 4096, N = 11008 (87, 71); 800 takes M = 192, K = N = 4096 from them (30 us, 25).
+            const double group = wide ? 830.0 + 1.67 * tn : 700.0;
             double t = (double)waves * ((double)((G + ks - 1) / ks) * group + 1500.0 + 33.0 * tn);
             if (ks > 1) t += 4000.0 + (double)ks * (double)M * (double)N * (gated ? 2 : 1) * 8.0 / 3000.0;
             if (best_t < 0.0 || t < best_t) {
