@@ -632,3 +632,11 @@ def test_launches_wait_for_whatever_precedes_them(M):
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     ok()
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 11008, 2176), (33, 11008, 4096), (40, 10000, 1152), (64, 5504, 7552), (24, 20000, 1024)])
+def test_tiles_cut_into_equal_shares(M, N, K):
+    """Small batches whose tiles do not fill whole waves: shares that end inside tiles, odd group counts."""
+    fused_case(M, N, K, "gelu", True, True, True)
+    gated_case(M, N // 16 * 8, K, "silu", True)
+    ok()

@@ -40,6 +40,7 @@
 //
 // Few tiles: K is cut into slices of whole groups, their fp32 sums go to the workspace [slice][layer]
 // [M][N] and ffn_reduce_kernel adds them in slice order and runs the epilogue: deterministic.
+// Small batches with a nearly empty last wave: equal shares of all tiles' steps instead (FgShares).
 //
 // Every mbarrier wait is bounded; on timeout the kernel records W4_ERR_DEVICE_TIMEOUT and drains.
 #include <algorithm>
@@ -84,6 +85,19 @@ struct FgCfg {
     static_assert(kNB * kGPS * NMAX + (kWide ? 0 : 64 * kAG * kGPS) <= 512, "TMEM");
 };
 
+// Small batches whose tiles leave a last wave nearly empty: the steps of all tiles laid end to end and
+// cut into equal shares, one per CTA.  A tile that lies in one share is finished there; the parts of
+// the others go to the workspace, in the order of their steps, and ffn_reduce_kernel adds them.
+struct FgShares {
+    int ctas;   // shares; 0: none
+    int steps;  // of a tile
+    int total;  // of all tiles; total * ctas < 2^29
+    __host__ __device__ int start(int c) const { return c * total / ctas; }
+    __host__ __device__ int owner(int step) const { return ((step + 1) * ctas - 1) / total; }
+    __host__ __device__ int first(int tile) const { return owner(tile * steps); }
+    __host__ __device__ int parts(int tile) const { return owner(tile * steps + steps - 1) - first(tile) + 1; }
+};
+
 struct FgArgs {
     const unsigned short* s0;
     const uint8_t* z0;
@@ -99,6 +113,7 @@ struct FgArgs {
     int M, N, G;
     int tn;           // X rows per tile
     FfnRaster raster;  // ks: slices of K
+    FgShares shares;
     int units;
     int stages;
     int vec;          // metadata rows allow 4-group vector loads
@@ -117,9 +132,21 @@ struct FgUnit {
     int m0, nt, slice, g0, g1;
 };
 
+// A share's tiles are its CTA's units in turn (u = share + i * ctas); those past its end are empty.
+template <bool SHARES>
 __device__ __forceinline__ FgUnit fg_unit(const FgArgs& p, int u) {
-    const FfnUnit t = ffn_unit(p.raster, u);
     FgUnit r;
+    if (SHARES && p.shares.ctas) {
+        const FgShares& h = p.shares;
+        const int c = u % h.ctas, begin = h.start(c), end = h.start(c + 1);
+        r.nt = begin / h.steps + u / h.ctas;
+        r.m0 = 0;
+        r.slice = c - h.first(r.nt);
+        r.g0 = 2 * max(begin - r.nt * h.steps, 0);
+        r.g1 = max(min(2 * (end - r.nt * h.steps), p.G), r.g0);
+        return r;
+    }
+    const FfnUnit t = ffn_unit(p.raster, u);
     r.slice = t.slice;
     r.nt = t.nt;
     r.m0 = t.mt * p.tn;
@@ -348,7 +375,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
             int ahead = 0;
             if (p.early) {  // the first ring's weights, before the preceding kernel has finished
                 for (int u = cluster; u < p.units && ahead < S; u += n_clusters) {
-                    const FgUnit w = fg_unit(p, u);
+                    const FgUnit w = fg_unit<!C::kWide>(p, u);
                     for (int g = w.g0; g < w.g1 && ahead < S; g += GPS, ++ahead) {
                         if (elect_one()) load_w(w, g, min(GPS, w.g1 - g), ahead);
                         __syncwarp();
@@ -360,7 +387,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
             uint32_t ph = 1;
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
-                const FgUnit w = fg_unit(p, u);
+                const FgUnit w = fg_unit<!C::kWide>(p, u);
                 const int mx = w.m0 + (int)rank * xrows;
                 for (int g = w.g0; g < w.g1; g += GPS, ++it) {
                     if (it >= ahead && !mbar_wait_long(done_bar(s), ph, abort_flag)) { fail(); ok = false; break; }
@@ -392,7 +419,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
             int it = 0, s = 0;
             bool ok = true;
             for (int u = cluster; u < p.units && ok; u += n_clusters) {
-                const FgUnit w = fg_unit(p, u);
+                const FgUnit w = fg_unit<!C::kWide>(p, u);
                 for (int g = w.g0; g < w.g1; g += GPS, ++it) {
                     const int b = it % NB, a = it % AG;
                     // the fold of the step NB ago usually comes last: it is waited for last
@@ -448,7 +475,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
         int it = 0, s = 0, sa = 0;  // step, its ring stage, the ring stage of step it - AG (S >= AG)
         uint32_t ph = 0, pa = 0;
         for (int u = cluster; u < p.units; u += n_clusters) {
-            const FgUnit w = fg_unit(p, u);
+            const FgUnit w = fg_unit<!C::kWide>(p, u);
             const int n = w.nt * TN + (GATED ? (int)rank * 64 + 16 * q + (lane & 15) : (int)rank * 128 + r);
             const bool nv = n < p.N;
             const uint8_t* zrow = zbase + (int64_t)(nv ? n : 0) * p.G;
@@ -550,7 +577,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
         int b = 0, s = 0;  // TMEM buffer and ring stage of the group
         uint32_t ph = 0;
         for (int u = cluster; u < p.units; u += n_clusters) {
-            const FgUnit w = fg_unit(p, u);
+            const FgUnit w = fg_unit<!C::kWide>(p, u);
             const int n = w.nt * TN + (GATED ? (int)rank * 64 + 16 * q + (lane & 15) : (int)rank * 128 + r);
             const bool nv = n < p.N;
             const unsigned short* srow = sbase_row + (int64_t)(nv ? n : 0) * p.G;
@@ -618,9 +645,10 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                 }
                 if (++b == NB) b = 0;
             }
+            if (!C::kWide && w.g0 == w.g1) continue;  // past the end of the CTA's share
             if (wg_barrier_any(1 + f, !ok)) continue;  // all four warps agree before the staging barriers
             const int m0 = w.m0 + f * ncol;
-            if (p.P) {
+            if (p.P && (C::kWide || !p.shares.ctas || w.g1 - w.g0 < p.G)) {
                 float* P = p.P + ((int64_t)w.slice * (GATED ? 2 : 1) + (GATED && upper ? 1 : 0)) * p.M * p.N;
 #pragma unroll
                 for (int c = 0; c < NACC; c += 2) {
@@ -648,15 +676,20 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
 }
 
 // The K slices' partial sums [slice][layer][M][N] added in slice order, then the epilogue.  No
-// slices (an empty K): the epilogue of zeros.  Launched as a programmatic dependent of the kernel
-// that writes the partials.
+// slices (an empty K): the epilogue of zeros.  With shares: only the tiles (of `rows` outputs n) that were
+// cut, from as many parts as each has.  Launched as a programmatic dependent of the kernel that writes
+// the partials.
 template <int ACT, bool GATED>
-__global__ void __launch_bounds__(256) ffn_reduce_kernel(const float* P, int slices, int64_t mn, int N, const __half* bias,
+__global__ void __launch_bounds__(256) ffn_reduce_kernel(const float* P, int slices, FgShares shares, int rows, int64_t mn, int N, const __half* bias,
                                                          const __half* residual, __half* Y, __half* Z, __half* U) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr int L = GATED ? 2 : 1;
     for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < mn; e += (int64_t)gridDim.x * 1024) {
+        if (shares.ctas) {
+            slices = shares.parts((int)(e % N) / rows);
+            if (slices == 1) continue;
+        }
         float4 a[L];
 #pragma unroll
         for (int l = 0; l < L; ++l) a[l] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -695,6 +728,8 @@ __global__ void __launch_bounds__(256) ffn_reduce_kernel(const float* P, int sli
 struct FgPlan {
     int tn, ks, stages, m_tiles, n_tiles, units;
     bool wide;  // the 256-column instantiation
+    int parts;  // partial sums of an output at most: ks, or of the shares
+    FgShares shares;
     uint32_t smem;
 };
 
@@ -728,7 +763,29 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
                 best.m_tiles = (int)m_tiles;
                 best.n_tiles = (int)n_tiles;
                 best.units = (int)units;
+                best.parts = ks;
+                best.shares = {};
             }
+        }
+        // shares: one for each SM, with a fill and an epilogue for each tile that a share touches, and its
+        // first and last tile's partial sums written and read
+        // (M = 32: gated K = 8192, N = 28672 123 us in whole tiles, 103 in shares; gated K = 4096, N = 11008
+        // 39, 34; plain K = 28672, N = 8192 64 in two slices, 60 in shares; where the rule is near its edge
+        // either is up to 2 us better)
+        const int64_t steps = (G + 1) / 2, total = n_tiles * steps, len = total / sms;
+        if (wide || m_tiles > 1 || len < 4 || total * sms >= (1ll << 29)) continue;
+        const int64_t longest = (total + sms - 1) / sms, per = (longest + steps - 2) / steps + 1;
+        const double t = (double)longest * 1400.0 + (double)per * (1500.0 + 33.0 * tn) + 4000.0 +
+                         (double)sms * 2.0 * 128.0 * (double)M * 8.0 / 3000.0;
+        if (t < best_t) {
+            best_t = t;
+            best.tn = tn;
+            best.ks = 1;
+            best.m_tiles = 1;
+            best.n_tiles = (int)n_tiles;
+            best.units = (int)(sms * per);
+            best.parts = (int)((steps + len - 1) / len + 1);
+            best.shares = {(int)sms, (int)steps, (int)total};
         }
     }
     best.wide = best.tn > 64;
@@ -779,11 +836,10 @@ cudaError_t fg_launch(const CUtensorMap& tx, const CUtensorMap& t0, const CUtens
     return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<GATED, NMAX>, tx, t0, t1, args);
 }
 
-}  // namespace
-
-cudaError_t launch_ffn_reduce(const float* P, int slices, int64_t M, int64_t N, bool gated, const W4Epilogue& ep,
-                              cudaStream_t stream) {
+cudaError_t fg_reduce(const float* P, int slices, const FgShares& shares, int64_t M, int64_t N, bool gated, const W4Epilogue& ep,
+                      cudaStream_t stream) {
     const int64_t mn = M * N;
+    const int rows = gated ? 64 : 128;  // outputs n of a shared tile
     const int64_t want = (mn / 4 + 255) / 256, cap = (int64_t)device_sm_count() * 8;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min(want, cap), 1, 1);
@@ -797,23 +853,30 @@ cudaError_t launch_ffn_reduce(const float* P, int slices, int64_t M, int64_t N, 
     return dispatch_act(ep.activation, [&](auto act) {
         constexpr int ACT = decltype(act)::value;
         if (gated)
-            return cudaLaunchKernelEx(&cfg, ffn_reduce_kernel<ACT, true>, P, slices, mn, (int)N, hp(ep.bias),
+            return cudaLaunchKernelEx(&cfg, ffn_reduce_kernel<ACT, true>, P, slices, shares, rows, mn, (int)N, hp(ep.bias),
                                       hp(ep.residual), hp(ep.Y), hp(ep.Z), hp(ep.U));
-        return cudaLaunchKernelEx(&cfg, ffn_reduce_kernel<ACT, false>, P, slices, mn, (int)N, hp(ep.bias), hp(ep.residual),
+        return cudaLaunchKernelEx(&cfg, ffn_reduce_kernel<ACT, false>, P, slices, shares, rows, mn, (int)N, hp(ep.bias), hp(ep.residual),
                                   hp(ep.Y), hp(ep.Z), hp(ep.U));
     });
 }
 
+}  // namespace
+
+cudaError_t launch_ffn_reduce(const float* P, int slices, int64_t M, int64_t N, bool gated, const W4Epilogue& ep,
+                              cudaStream_t stream) {
+    return fg_reduce(P, slices, {}, M, N, gated, ep, stream);
+}
+
 size_t ffn_gemm_workspace(int64_t M, int64_t N, int64_t K, bool gated) {
     const FgPlan pl = fg_plan(M, N, K, gated);
-    return pl.ks > 1 ? (size_t)pl.ks * (size_t)M * (size_t)N * (gated ? 8 : 4) : 0;
+    return pl.parts > 1 ? (size_t)pl.parts * (size_t)M * (size_t)N * (gated ? 8 : 4) : 0;
 }
 
 cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2,
                             const W4Epilogue& ep, void* ws, bool weights_static, int* status, cudaStream_t stream) {
     const bool gated = w2 != nullptr;
     const FgPlan pl = fg_plan(M, N, K, gated);
-    if (pl.ks > 1 && !ws) return cudaErrorInvalidValue;
+    if (pl.parts > 1 && !ws) return cudaErrorInvalidValue;
     CUtensorMap tx, t0, t1;
     if (!make_tensor_map_2d(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)K, (uint64_t)M, 64,
                             (uint32_t)(pl.wide ? pl.tn / 2 : pl.tn),
@@ -842,7 +905,7 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
     a.Y = hp(ep.Y);
     a.Z = hp(ep.Z);
     a.U = hp(ep.U);
-    a.P = pl.ks > 1 ? static_cast<float*>(ws) : nullptr;
+    a.P = pl.parts > 1 ? static_cast<float*>(ws) : nullptr;
     a.act = ep.activation;
     a.M = (int)M;
     a.N = (int)N;
@@ -853,6 +916,7 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
     a.raster.ks = pl.ks;
     // m-tiles whose X stays in L2 (about 48 MB) run down the weights together
     a.raster.gm = (int)std::max<int64_t>(1, std::min<int64_t>(pl.m_tiles, (48ll << 20) / ((int64_t)pl.tn * K * 2)));
+    a.shares = pl.shares;
     a.units = pl.units;
     a.stages = pl.stages;
     a.vec = vec_ok(w) && (!gated || vec_ok(*w2)) ? 1 : 0;
@@ -861,8 +925,8 @@ cudaError_t launch_ffn_gemm(const uint16_t* X, int64_t M, int64_t N, int64_t K, 
     cudaError_t e;
     if (gated) e = pl.wide ? fg_launch<true, 256>(tx, t0, t1, a, pl, stream) : fg_launch<true, 64>(tx, t0, t1, a, pl, stream);
     else e = pl.wide ? fg_launch<false, 256>(tx, t0, t1, a, pl, stream) : fg_launch<false, 64>(tx, t0, t1, a, pl, stream);
-    if (e != cudaSuccess || pl.ks == 1) return e;
-    return launch_ffn_reduce(a.P, pl.ks, M, N, gated, ep, stream);
+    if (e != cudaSuccess || pl.parts == 1) return e;
+    return fg_reduce(a.P, pl.ks, pl.shares, M, N, gated, ep, stream);
 }
 
 }  // namespace w4
