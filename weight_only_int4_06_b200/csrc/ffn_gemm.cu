@@ -17,8 +17,9 @@
 //             Weights in tensor memory would spare the port 64 KB but leave columns for 192 rows of X only,
 //             whose group took 1152 cycles where 256 take 1258: slower by a fifth.
 //   NMAX 64   small batches: one CTA, 128 weight rows by up to 64 rows of X, the weights in tensor memory,
-//             two groups a step.  Bound by instruction issue, half of it the dequantisation's: 57 us at
-//             M = 32, K = 28672, N = 8192, where HBM would allow 19.
+//             two groups a step.  Bound by the chain of a step (codes in, dequantised, stored to tensor
+//             memory, multiplied, read back; two in flight): 900 cycles a group, of which the dequantisation
+//             keeps the ALU pipe busy for 390, where HBM would allow 370; 55 us at M = 32, K = 28672, N = 8192.
 // At M = 2048, K = 4096, N = 11008: gated 291 us (1270 TFLOP/s), plain 150 us.
 //
 //   warp 0       TMA producer of its CTA: X (boxes of 64 k) and the packed rows of a step
