@@ -74,7 +74,7 @@ struct FgCfg {
     static constexpr bool kWide = NMAX > 64;
     static constexpr int kCtas = kWide ? 2 : 1;     // CTAs that share a tile
     static constexpr int kGPS = kWide ? 1 : 2;      // groups per step
-    static constexpr int kDW = kGPS;                // dequantising warpgroups: one to each group of a step
+    static constexpr int kDW = kWide ? 1 : 2;       // dequantising warpgroups, taking the steps in turn
     static constexpr int kNB = 2;                   // steps whose sums TMEM holds
     static constexpr int kAG = 2;                   // dequantised steps
     static constexpr int kThreads = 128 * (1 + kDW + 2);
@@ -292,7 +292,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                     const __grid_constant__ CUtensorMap tmW1, const FgArgs p) {
     using C = FgCfg<NMAX>;
     constexpr int NACC = NMAX / 2;            // columns per fold thread
-    constexpr int NB = C::kNB, AG = C::kAG, GPS = C::kGPS, CTAS = C::kCtas;
+    constexpr int NB = C::kNB, AG = C::kAG, GPS = C::kGPS, DW = C::kDW, CTAS = C::kCtas;
     constexpr int TROWS = 128 * CTAS;         // weight rows of a tile
     constexpr int TN = GATED ? TROWS / 2 : TROWS;  // outputs n of a tile; TN / CTAS in each CTA
     constexpr int FOLD_WARP = 4 + 4 * C::kDW;
@@ -323,7 +323,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
             mbar_init(full_bar(s), 1);
             mbar_init(done_bar(s), 1);
         }
-        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 4 * CTAS * GPS);  // a warpgroup of each CTA for each group
+        for (int i = 0; i < AG; ++i) mbar_init(a_full(i), 4 * CTAS);  // a warpgroup of each CTA
         for (int i = 0; i < NB; ++i) mbar_init(d_empty(i), 8 * CTAS);  // eight fold warps of each CTA
         *abort_flag = 0;
         fence_mbarrier_init();
@@ -462,15 +462,15 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
     } else if (warp < FOLD_WARP) {
         regs_dec<C::kRegsDeq>();
         // ------------------------------------------------------------ dequantisation
+        // a warpgroup takes every DW-th step: while one waits (for codes, its slot, its stores), another computes
         const int wg = (warp - 4) >> 2, q = warp & 3;
-        const int j = wg;  // its group of every step
         const int r = q * 32 + lane;  // row of the CTA's 128 = TMEM lane
         // TMA swizzle of the row's 16-byte pieces: 64-byte rows by bits 1-2 of the row, 128-byte ones by 0-2
         const uint32_t sw = GPS == 1 ? (uint32_t)(r >> 1) & 3 : (uint32_t)r & 7;
         const uint32_t c0 = p_off + (uint32_t)r * (64 * GPS);
         const uint8_t* zbase = GATED && lane >= 16 ? p.z1 : p.z0;
         const uint32_t remote = CTAS == 2 ? map_shared(a_full(0), 0) : a_full(0);
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol + (uint32_t)j * 64;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + C::kACol;
         pdl_wait();  // no bounded wait runs beside the preceding kernel
         bool ok = true;
         int it = 0, s = 0, sa = 0;  // step, its ring stage, the ring stage of step it - AG (S >= AG)
@@ -480,76 +480,80 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
             const int n = w.nt * TN + (GATED ? (int)rank * 64 + 16 * q + (lane & 15) : (int)rank * 128 + r);
             const bool nv = n < p.N;
             const uint8_t* zrow = zbase + (int64_t)(nv ? n : 0) * p.G;
-            uint32_t z4 = nv && w.g0 + j < w.g1 ? fg_zeros4(zrow, w.g0 + j, p.G, p.vec) : 0, z4n = 0;
-            int zb = (w.g0 + j) & ~3;  // z4 holds groups zb ... zb + 3, z4n the next four
+            const int gf = w.g0 + GPS * ((wg + it) % DW);  // this warpgroup's first group (DW <= 2: wg - it = wg + it)
+            uint32_t z4 = nv && gf < w.g1 ? fg_zeros4(zrow, gf, p.G, p.vec) : 0, z4n = 0;
+            int zb = gf & ~3;  // z4 holds groups zb ... zb + 3, z4n the next four
             if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
             for (int gs = w.g0; gs < w.g1; gs += GPS, ++it) {
-                const int g = gs + j;  // past the last group of an odd count: dequantised all the same, not multiplied
-                if ((g & ~3) != zb) {  // the next four groups' zero points are fetched while these are used
-                    z4 = z4n;
-                    zb = g & ~3;
-                    if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
+                auto next_stage = [&]() {
+                    if (it >= AG && ++sa == S) { sa = 0; pa ^= 1; }
+                    if (++s == S) { s = 0; ph ^= 1; }
+                };
+                if (DW > 1 && it % DW != wg) {
+                    next_stage();
+                    continue;
                 }
-                const uint32_t z = (z4 >> (8 * (g & 3))) & 0xFFu;
-                // A byte in both halves of a word, the low nibble kept in the lower and the high one in the
-                // upper, under the exponent of 1024: the pair 1024 + q, 1024 + 16 q'.  Then (1024 + q) * 1 - (1024
-                // + z) and (1024 + 16 q') / 16 - (64 + z): q - z and q' - z, exact.  Three instructions a pair.
-                const uint32_t zadd = (0xE400u + z) | ((0xD400u | (z << 4)) << 16);
                 const uint32_t slot = (uint32_t)(it % AG);
-                // two of the row's four 16-byte pieces: half h of the group's codes
-                auto load = [&](int h, uint32_t (&words)[8]) {
+                // two of the row's four 16-byte pieces: half h of group j's codes
+                auto load = [&](int j, int h, uint32_t (&words)[8]) {
                     const unsigned char* st = smem + (uint32_t)s * stage_bytes + c0;
                     const uint4 a = *reinterpret_cast<const uint4*>(st + (((4 * j + 2 * h) ^ sw) << 4));
                     const uint4 b = *reinterpret_cast<const uint4*>(st + (((4 * j + 2 * h + 1) ^ sw) << 4));
                     words[0] = a.x; words[1] = a.y; words[2] = a.z; words[3] = a.w;
                     words[4] = b.x; words[5] = b.y; words[6] = b.z; words[7] = b.w;
                 };
-                auto dequant = [&](uint32_t wd, uint32_t (&o)[4]) {
-                    o[0] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x0000), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
-                    o[1] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x1111), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
-                    o[2] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x2222), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
-                    o[3] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x3333), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
+                auto free_slot = [&]() {  // the step that used this slot AG steps ago has been multiplied
+                    if (it >= AG && ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
                 };
                 if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
                 uint32_t words[8];
-                load(0, words);
+                load(0, 0, words);
                 uint32_t next[8];
-                if (C::kWide) load(1, next);
-                auto free_slot = [&]() {  // the step that used this slot AG steps ago has been multiplied
-                    if (it >= AG) {
-                        if (ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
-                        if (++sa == S) { sa = 0; pa ^= 1; }
+                if (C::kWide) {
+                    load(0, 1, next);
+                    free_slot();
+                }
+#pragma unroll
+                for (int j = 0; j < GPS; ++j) {
+                    const int g = gs + j;
+                    if (j > 0 && g >= w.g1) break;
+                    if ((g & ~3) != zb) {  // the next four groups' zero points are fetched while these are used
+                        z4 = z4n;
+                        zb = g & ~3;
+                        if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
                     }
-                };
-                if (C::kWide) free_slot();
+                    const uint32_t z = (z4 >> (8 * (g & 3))) & 0xFFu;
+                    // A byte in both halves of a word, the low nibble kept in the lower and the high one in the
+                    // upper, under the exponent of 1024: the pair 1024 + q, 1024 + 16 q'.  Then (1024 + q) * 1 - (1024
+                    // + z) and (1024 + 16 q') / 16 - (64 + z): q - z and q' - z, exact.  Three instructions a pair.
+                    const uint32_t zadd = (0xE400u + z) | ((0xD400u | (z << 4)) << 16);
+                    auto dequant = [&](uint32_t wd, uint32_t* o) {
+                        o[0] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x0000), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
+                        o[1] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x1111), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
+                        o[2] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x2222), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
+                        o[3] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x3333), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
+                    };
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (C::kWide) {
-                        unsigned char* row = smem + w0 + slot * C::kWBytes + (uint32_t)h * (C::kWBytes / 2) + (uint32_t)r * 128;
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (C::kWide) {
+                            unsigned char* row = smem + w0 + slot * C::kWBytes + (uint32_t)h * (C::kWBytes / 2) + (uint32_t)r * 128;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {  // 8-k chunks of the block of 64 k
-                            uint32_t o[4];
-                            dequant(words[c], o);
-                            *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            for (int c = 0; c < 8; ++c) {  // 8-k chunks of the block of 64 k
+                                uint32_t o[4];
+                                dequant(words[c], o);
+                                *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            }
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) words[c] = next[c];
+                        } else {
+                            uint32_t o[32];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) dequant(words[c], o + 4 * c);
+                            if (h == 0) load(j, 1, words);
+                            else if (j + 1 < GPS) load(j + 1, 0, words);
+                            if (j == 0 && h == 0) free_slot();
+                            if (ok) tmem_st_32x32b_x32(taddr + (slot * GPS + j) * 64 + h * 32, o);
                         }
-                    } else {
-                        uint32_t o[32];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            uint32_t o4[4];
-                            dequant(words[c], o4);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) o[4 * c + i] = o4[i];
-                        }
-                        if (h == 0) {
-                            load(1, words);
-                            free_slot();
-                        }
-                        if (ok) tmem_st_32x32b_x32(taddr + slot * (64 * GPS) + h * 32, o);
-                    }
-                    if (C::kWide && h == 0) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) words[c] = next[c];
                     }
                 }
                 if constexpr (C::kWide) {
@@ -560,7 +564,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                 }
                 __syncwarp();
                 if (ok && lane == 0) fg_arrive<CTAS>(remote + 8u * slot);
-                if (++s == S) { s = 0; ph ^= 1; }
+                next_stage();
             }
         }
     } else {
