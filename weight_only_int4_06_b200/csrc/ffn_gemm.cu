@@ -17,9 +17,9 @@
 //             Weights in tensor memory would spare the port 64 KB but leave columns for 192 rows of X only,
 //             whose group took 1152 cycles where 256 take 1258: slower by a fifth.
 //   NMAX 64   small batches: one CTA, 128 weight rows by up to 64 rows of X, the weights in tensor memory,
-//             two groups a step.  Bound by the chain of a step (codes in, dequantised, stored to tensor
-//             memory, multiplied, read back; two in flight): 900 cycles a group, of which the dequantisation
-//             keeps the ALU pipe busy for 390, where HBM would allow 370; 55 us at M = 32, K = 28672, N = 8192.
+//             two groups a step.  Bound by the dequantisation (a step's codes come in, are converted and
+//             stored to tensor memory; two steps in flight): 780 cycles a group, in 340 of which the ALU pipe
+//             converts, where HBM would allow 370; 48 us at M = 32, K = 28672, N = 8192.
 // At M = 2048, K = 4096, N = 11008: gated 291 us (1270 TFLOP/s), plain 150 us.
 //
 //   warp 0       TMA producer of its CTA: X (boxes of 64 k) and the packed rows of a step
@@ -505,6 +505,16 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                 auto free_slot = [&]() {  // the step that used this slot AG steps ago has been multiplied
                     if (it >= AG && ok && !warp_wait(done_bar(sa), pa, abort_flag)) { fail(); ok = false; }
                 };
+                auto zero_add = [&](int g) {  // -(1024 + z), -(64 + z)
+                    if ((g & ~3) != zb) {  // the next four groups' zero points are fetched while these are used
+                        z4 = z4n;
+                        zb = g & ~3;
+                        if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
+                    }
+                    const uint32_t z = (z4 >> (8 * (g & 3))) & 0xFFu;
+                    return (0xE400u + z) | ((0xD400u | (z << 4)) << 16);
+                };
+                uint32_t zadd = zero_add(gs);
                 if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
                 uint32_t words[8];
                 load(0, 0, words);
@@ -517,16 +527,10 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                 for (int j = 0; j < GPS; ++j) {
                     const int g = gs + j;
                     if (j > 0 && g >= w.g1) break;
-                    if ((g & ~3) != zb) {  // the next four groups' zero points are fetched while these are used
-                        z4 = z4n;
-                        zb = g & ~3;
-                        if (nv && zb + 4 < p.G) z4n = fg_zeros4(zrow, zb + 4, p.G, p.vec);
-                    }
-                    const uint32_t z = (z4 >> (8 * (g & 3))) & 0xFFu;
+                    if (j > 0) zadd = zero_add(g);
                     // A byte in both halves of a word, the low nibble kept in the lower and the high one in the
                     // upper, under the exponent of 1024: the pair 1024 + q, 1024 + 16 q'.  Then (1024 + q) * 1 - (1024
                     // + z) and (1024 + 16 q') / 16 - (64 + z): q - z and q' - z, exact.  Three instructions a pair.
-                    const uint32_t zadd = (0xE400u + z) | ((0xD400u | (z << 4)) << 16);
                     auto dequant = [&](uint32_t wd, uint32_t* o) {
                         o[0] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x0000), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
                         o[1] = hfma2_u32(lop3_and_or(__byte_perm(wd, 0, 0x1111), 0x00F0000Fu, 0x64006400u), 0x2C003C00u, zadd);
@@ -740,6 +744,7 @@ struct FgPlan {
 
 FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
     const int64_t sms = std::max(2, device_sm_count()), G = K / 128;
+    constexpr double kSmallGroup = 630.0;
     FgPlan best = {};
     double best_t = -1.0;
     for (int tn = 32; tn <= 256; tn += 32) {
@@ -754,11 +759,11 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
             const int64_t units = tiles * ks;
             const int64_t waves = (units + slots - 1) / slots;
             // cycles per group (measured: 1152 at tn = 192, 1258 at 256); per unit: filling and the epilogue (33
-            // per column); a second launch and its traffic when K is cut.  Small tiles: 880 a group measured
-            // with every SM at work, less with some idle; 700 chooses best between the two instantiations.
-            // 500 leaves M = 128, K = 28672, N = 8192 to small tiles (128 us, 100 in large ones) and the gated
-            // M = 256, K = 4096, N = 11008 (87, 71); 800 takes M = 192, K = N = 4096 from them (30 us, 25).
-            const double group = wide ? 830.0 + 1.67 * tn : 700.0;
+            // per column); a second launch and its traffic when K is cut.  Small tiles: 780 a group measured
+            // with the start and end of the kernel; 630 chooses best between the two instantiations.  700 gives
+            // M = 96, K = N = 4096 to large tiles (23.5 us, 19.5 in small ones) and the gated M = 96, K = 4096, N =
+            // 11008 (55, 51); 560 leaves the gated M = 192, K = 4096, N = 11008 to small ones (63, 61 in large).
+            const double group = wide ? 830.0 + 1.67 * tn : kSmallGroup;
             double t = (double)waves * ((double)((G + ks - 1) / ks) * group + 1500.0 + 33.0 * tn);
             if (ks > 1) t += 4000.0 + (double)ks * (double)M * (double)N * (gated ? 2 : 1) * 8.0 / 3000.0;
             if (best_t < 0.0 || t < best_t) {
@@ -780,7 +785,7 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
         const int64_t steps = (G + 1) / 2, total = n_tiles * steps, len = total / sms;
         if (wide || m_tiles > 1 || len < 4 || total * sms >= (1ll << 29)) continue;
         const int64_t longest = (total + sms - 1) / sms, per = (longest + steps - 2) / steps + 1;
-        const double t = (double)longest * 1400.0 + (double)per * (1500.0 + 33.0 * tn) + 4000.0 +
+        const double t = (double)longest * 2.0 * kSmallGroup + (double)per * (1500.0 + 33.0 * tn) + 4000.0 +
                          (double)sms * 2.0 * 128.0 * (double)M * 8.0 / 3000.0;
         if (t < best_t) {
             best_t = t;
