@@ -20,7 +20,7 @@
 //             two groups a step.  Bound by the dequantisation (a step's codes come in, are converted and
 //             stored to tensor memory; two steps in flight): 780 cycles a group, in 340 of which the ALU pipe
 //             converts, where HBM would allow 370; 48 us at M = 32, K = 28672, N = 8192.
-// At M = 2048, K = 4096, N = 11008: gated 291 us (1270 TFLOP/s), plain 150 us.
+// At M = 2048, K = 4096, N = 11008: gated 289 us (1280 TFLOP/s), plain 145 us.
 //
 //   warp 0       TMA producer of its CTA: X (boxes of 64 k) and the packed rows of a step
 //   warp 1       first CTA: issues the tcgen05.mma (N = tn, K = 16) and one commit a step
@@ -514,7 +514,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                     const uint32_t z = (z4 >> (8 * (g & 3))) & 0xFFu;
                     return (0xE400u + z) | ((0xD400u | (z << 4)) << 16);
                 };
-                uint32_t zadd = zero_add(gs);
+                uint32_t zadd = C::kWide ? zero_add(gs) : 0;  // before the wait: 1 % faster in large tiles, slower in small ones
                 if (ok && !warp_wait(full_bar(s), ph, abort_flag)) { fail(); ok = false; }
                 uint32_t words[8];
                 load(0, 0, words);
@@ -527,7 +527,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                 for (int j = 0; j < GPS; ++j) {
                     const int g = gs + j;
                     if (j > 0 && g >= w.g1) break;
-                    if (j > 0) zadd = zero_add(g);
+                    if (!C::kWide) zadd = zero_add(g);
                     // A byte in both halves of a word, the low nibble kept in the lower and the high one in the
                     // upper, under the exponent of 1024: the pair 1024 + q, 1024 + 16 q'.  Then (1024 + q) * 1 - (1024
                     // + z) and (1024 + 16 q') / 16 - (64 + z): q - z and q' - z, exact.  Three instructions a pair.
