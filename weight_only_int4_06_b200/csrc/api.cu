@@ -573,10 +573,9 @@ static cudaError_t zero_half(uint16_t* p, int64_t rows, int64_t cols, cudaStream
 }
 
 // The GEMV up to 8 activation rows where one launch serves the shape and can bulk-copy the metadata,
-// else the tensor-core product.  Measured on B200 (us, residual epilogue, graph of back-to-back calls),
-// GEMV vs tensor cores: M = 8, K = 4096, N = 11008 14.7 vs 20.4; K = 28672, N = 8192 41 vs 59; but M = 8,
-// K = 11008, N = 4096 in two launches of 4 rows 24.4 vs 19.4; M = 16 at those shapes 20.7 vs 20.4, 82 vs
-// 59 and 47.9 vs 19.4.
+// else the tensor-core product.  Measured on B200 (us, back-to-back calls), GEMV at M = 8 vs tensor cores
+// at M = 9, whose work is the same there: K = 4096, N = 11008 13.0 vs 17.8; K = 28672, N = 8192 39.6 vs 46.5.
+// Shapes that need two launches of the GEMV: M = 8, K = 11008, N = 4096 24.4 vs 16.0.
 static bool ffn_decode(int64_t M, int64_t N, int64_t K, const W4Layer& w, const W4Layer* w2) {
     auto meta_ok = [](const W4Layer& l) { return aligned16(l.scales) && aligned16(l.zeros); };
     return meta_ok(w) && (!w2 || meta_ok(*w2)) && decode_ffn_fits(M, N, K, w2 != nullptr);
