@@ -507,7 +507,8 @@ w4_status awq_clip_search(const uint16_t* X, int64_t T, const uint16_t* W, int64
  * products accumulate in fp32 and everything up to an output's one rounding to fp16 stays in fp32
  * (exceptions are stated at the call).  scales and zeros need no alignment; every other array is
  * 16-byte aligned, ws included.  An optional array is absent when its pointer is NULL.  Outputs
- * must not overlap inputs except where the call says so.  M, N or K may be zero: an empty sum is 0.
+ * must not overlap inputs except where the call says so.  M, N or K may be zero: an empty sum is 0,
+ * and an array without elements may be NULL.
  * N % 8 == 0, K % 128 == 0, group 128.  Calls on the same stream may share a workspace; calls that
  * may overlap on the GPU (other streams, two graphs replayed together) need one each.
  */

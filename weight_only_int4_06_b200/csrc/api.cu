@@ -683,9 +683,8 @@ w4_status w4_gemm_dx(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const 
     if (st == W4_OK) st = ws_check(need, ws, ws_bytes);
     if (st != W4_OK) return st;
     const W4Layer w = {packed, scales, zeros}, w2 = {packed2, scales2, zeros2};
-    if (two && (!dY2 || layer_null(w2))) return W4_ERR_NULL;
-    if (M == 0 || K == 0) return W4_OK;
-    if (!dX || (N > 0 && (!dY || layer_null(w)))) return W4_ERR_NULL;
+    if (M == 0 || K == 0) return W4_OK;  // no outputs: arrays without elements may be NULL
+    if (!dX || (N > 0 && (!dY || layer_null(w) || (two && (!dY2 || layer_null(w2)))))) return W4_ERR_NULL;
     if (!aligned16(dX) || (N > 0 && (!aligned16(dY) || !aligned16(packed) || !aligned16(dY2) || !aligned16(packed2))))
         return W4_ERR_ALIGN;
     int* status = device_status_ptr();
