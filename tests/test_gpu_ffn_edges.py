@@ -32,3 +32,22 @@ def test_input_gradient_of_an_empty_pair(M, N, K):
         dX = B.w4_gemm_dx(ones(M, N), *zero_layer(N, K), dY2=ones(M, N), weights2=zero_layer(N, K), out=ones(M, K), **k)
         assert dX.shape == (M, K) and not dX.any()
     ok()
+
+
+@pytest.mark.parametrize("M,N", [(0, 16), (5, 0), (0, 0)])
+def test_gated_activation_backward_of_an_empty_batch(M, N):
+    """An empty U is still a U: a pair comes back, the outputs given are the ones returned, and it does not
+    go with a bias gradient."""
+    for k in halves():
+        dG, dU = B.w4_act_backward(ones(M, N), ones(M, N), U=ones(M, N), **k)
+        assert dG.shape == dU.shape == (M, N)
+        out = ones(M, N), ones(M, N)
+        got = B.w4_act_backward(ones(M, N), ones(M, N), U=ones(M, N), out=out, **k)
+        assert got[0] is out[0] and got[1] is out[1]
+        with pytest.raises(ValueError):
+            B.w4_act_backward(ones(M, N), ones(M, N), U=ones(M, N), out=(out[0], ones(M + 1, N + 8)), **k)
+        with pytest.raises(B.W4Error):
+            B.w4_act_backward(ones(M, N), ones(M, N), U=ones(M, N), bias_grad=True, **k)
+        dZ, db = B.w4_act_backward(ones(M, N), ones(M, N), bias_grad=True, **k)
+        assert dZ.shape == (M, N) and db.shape == (N,) and not db.any()
+    ok()

@@ -292,20 +292,22 @@ PyObject* act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* dY = x.first(0, M, N);
         if (!dY) return not_usual();
         const uint16_t *Z = x.optional(1, M, N), *U = x.optional(2, M, N);
+        const bool gated = !x.none(2);  // by the argument: an empty tensor has no address
         const int64_t act = x.integer(3), bias = x.integer(4);
+        if (x.ok && gated && bias) return PyLong_FromLong(W4_ERR_UNSUPPORTED);
         size_t need = 0;
         if (!x.ok || (bias && abi.act_ws(M, N, &need) != W4_OK)) return not_usual();
         Workspace ws;
         Out dZ, dU;
         at::Tensor db;
-        if ((bias && !ws.take(x, a[7], need)) || !dZ.take(x, a[5], M, N) || (U && !dU.take(x, a[6], M, N)))
+        if ((bias && !ws.take(x, a[7], need)) || !dZ.take(x, a[5], M, N) || (gated && !dU.take(x, a[6], M, N)))
             return not_usual();
         if (bias) db = at::empty({N}, at::TensorOptions().dtype(at::kFloat).device(x.dev));
         const w4_status st = abi.act_backward(static_cast<const uint16_t*>(dY->data_ptr()), Z, U, M, N, (int)act, h(dZ.t),
-                                              U ? h(dU.t) : nullptr, bias ? static_cast<float*>(db.data_ptr()) : nullptr, ws.p,
+                                              gated ? h(dU.t) : nullptr, bias ? static_cast<float*>(db.data_ptr()) : nullptr, ws.p,
                                               ws.bytes, stream_of(x));
         if (st != W4_OK) return PyLong_FromLong(st);
-        if (U) return wrap_tuple(dZ.t, dU.t);
+        if (gated) return wrap_tuple(dZ.t, dU.t);
         return bias ? wrap_tuple(dZ.t, db) : wrap(dZ.t);
     });
 }

@@ -14,7 +14,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libw4a16.so")
 
-W4_OK = 0
+W4_OK, W4_ERR_UNSUPPORTED = 0, 4
 STATUS_NAMES = {
     0: "W4_OK", 1: "W4_ERR_NULL", 2: "W4_ERR_SHAPE", 3: "W4_ERR_ALIGN", 4: "W4_ERR_UNSUPPORTED",
     5: "W4_ERR_WORKSPACE", 6: "W4_ERR_CUDA", 7: "W4_ERR_DEVICE_TIMEOUT", 8: "W4_ERR_RANGE",
@@ -897,6 +897,8 @@ def w4_act_backward(dY: torch.Tensor, Z: torch.Tensor | None, U: torch.Tensor | 
     yp = _arg(dY, torch.float16, (M, N), dev, "dY")
     zp = _arg(Z, torch.float16, (M, N), dev, "Z") if Z is not None else None
     up = _arg(U, torch.float16, (M, N), dev, "U") if U is not None else None
+    if U is not None and bias_grad:  # the C call takes an empty U for none
+        raise W4Error(W4_ERR_UNSUPPORTED, "w4_act_backward")
     if U is None:
         out = (out, None)
     elif out is None:
