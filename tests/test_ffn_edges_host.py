@@ -35,3 +35,20 @@ def test_input_gradient_of_a_pair_given_in_part(L):
         part = second[:i] + [None] + second[i + 1:]
         for s in (part, [GOOD if p is None else None for p in part]):
             assert L.w4_gemm_dx(GOOD, 4, 16, 256, GOOD, GOOD, GOOD, *s, 128, GOOD, GOOD, 1 << 40, None) == NULL
+
+
+def test_workspace_size_is_that_of_the_call_at_hand(monkeypatch):
+    """The plans depend on the current device's SM count: a size found on one device is not kept for another."""
+    sizes = iter((0, 4096, 64))
+
+    class Lib:
+        @staticmethod
+        def w4_gemm_fused_workspace_size(M, N, K, group, out):
+            out._obj.value = next(sizes)
+            return OK
+
+    monkeypatch.setattr(B, "lib", lambda: Lib)
+    like = torch.empty(0, dtype=torch.float16)
+    for need in (0, 4096, 64):
+        address, have, tensor = B._ffn_workspace("w4_gemm_fused_workspace_size", (4, 16, 256, 128), None, like)
+        assert have == need and (tensor is None) == (need == 0)

@@ -695,19 +695,12 @@ def _done(r, where: str):
     return r
 
 
-_ffn_ws_cache: dict = {}
-
-
 def _ffn_workspace(name: str, dims: tuple, workspace, like: torch.Tensor):
     """(address, bytes) of the caller's workspace or, where it has none or one too small, of a new
     one, and the tensor that holds it."""
-    need = _ffn_ws_cache.get((name, dims))
-    if need is None:
-        n = ctypes.c_size_t(0)
-        _check(getattr(lib(), name)(*dims, ctypes.byref(n)), name)
-        if len(_ffn_ws_cache) >= 4096:  # ragged batches: every M is a key
-            _ffn_ws_cache.clear()
-        need = _ffn_ws_cache[(name, dims)] = n.value
+    n = ctypes.c_size_t(0)
+    _check(getattr(lib(), name)(*dims, ctypes.byref(n)), name)
+    need = n.value
     if workspace is not None:
         if workspace.device != like.device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
