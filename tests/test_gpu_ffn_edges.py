@@ -51,3 +51,23 @@ def test_gated_activation_backward_of_an_empty_batch(M, N):
         dZ, db = B.w4_act_backward(ones(M, N), ones(M, N), bias_grad=True, **k)
         assert dZ.shape == (M, N) and db.shape == (N,) and not db.any()
     ok()
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 4, -2 ** 32, 2 ** 64, 2 ** 70, -2 ** 70])
+def test_codes_beyond_an_int_are_refused(value):
+    """activation, group and flags are C ints: a value whose low 32 bits are a valid code is still none."""
+    N, K = 16, 128
+    x, y, w = ones(2, K), ones(2, N), zero_layer(N, K)
+    calls = [lambda **k: B.w4_gemm_fused(x, *w, activation=value, **k), lambda **k: B.w4_gemm_fused(x, *w, group=value + 128, **k),
+             lambda **k: B.w4_gemm_fused(x, *w, flags=value, **k), lambda **k: B.w4_gemm_gated(x, w, w, activation=value, **k),
+             lambda **k: B.w4_gemm_gated(x, w, w, group=value + 128, **k), lambda **k: B.w4_gemm_gated(x, w, w, flags=value, **k),
+             lambda **k: B.w4_gemm_dx(y, *w, group=value + 128, **k),
+             lambda **k: B.w4_gemm_dx_gated(y, *w, x, x, activation=value, **k),
+             lambda **k: B.w4_gemm_dx_gated(y, *w, x, x, group=value + 128, **k),
+             lambda **k: B.w4_act_backward(y, y, activation=value, **k)]
+    for k in halves():
+        for call in calls:
+            with pytest.raises(B.W4Error):
+                call(**k)
+    assert torch.equal(B.w4_gemm_fused(x, *w, save_pre=2 ** 70)[1], B.w4_gemm_fused(x, *w))  # a truth value
+    ok()

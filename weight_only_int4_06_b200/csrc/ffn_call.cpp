@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <climits>
 #include <cstring>
 
 #include "w4a16.h"
@@ -39,10 +40,11 @@ struct Args {
 
     bool none(int i) const { return a[i] == Py_None; }
     int64_t integer(int i) {
-        if (PyLong_CheckExact(a[i])) return PyLong_AsLongLong(a[i]);
         if (PyBool_Check(a[i])) return a[i] == Py_True;
-        ok = false;
-        return 0;
+        int overflow = 0;
+        const long long v = PyLong_CheckExact(a[i]) ? PyLong_AsLongLongAndOverflow(a[i], &overflow) : LLONG_MAX;
+        if (overflow || v < INT_MIN || v > INT_MAX) ok = false;  // the C calls take an int
+        return ok ? v : 0;
     }
     const at::Tensor* tensor(PyObject* o) {
         if (ok && THPVariable_CheckExact(o)) return &THPVariable_Unpack(o);

@@ -631,6 +631,12 @@ def _arg(t: torch.Tensor, dtype, shape, dev, name) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
+def _code(value, where: str):
+    """Refuses an activation, group or flags argument that is no C int (ctypes would take its low 32 bits)."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise W4Error(W4_ERR_UNSUPPORTED, where)
+
+
 def _matrix(t: torch.Tensor, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
@@ -753,6 +759,8 @@ def w4_gemm_fused(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, z
         with other:
             return w4_gemm_fused(X, packed, scales, zeros, bias, activation, residual, save_pre, group, out, workspace,
                                  flags)
+    for c in (activation, group, flags):
+        _code(c, "w4_gemm_fused")
     xp = _arg(X, torch.float16, (M, K), dev, "X")
     w = _layer_args(packed, scales, zeros, N, K, group, dev, "")
     bp = _arg(bias, torch.float16, (N,), dev, "bias") if bias is not None else None
@@ -787,6 +795,8 @@ def w4_gemm_gated(X: torch.Tensor, gate, up, activation: int = ACT_SILU, save_pr
     if other is not None:
         with other:
             return w4_gemm_gated(X, gate, up, activation, save_pre, group, out, workspace, flags)
+    for c in (activation, group, flags):
+        _code(c, "w4_gemm_gated")
     xp = _arg(X, torch.float16, (M, K), dev, "X")
     g = _layer_args(*gate, N, K, group, dev, "gate ")
     u = _layer_args(*up, N, K, group, dev, "up ")
@@ -820,6 +830,7 @@ def w4_gemm_dx(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
     if other is not None:
         with other:
             return w4_gemm_dx(dY, packed, scales, zeros, dY2, weights2, group, out, workspace)
+    _code(group, "w4_gemm_dx")
     yp = _arg(dY, torch.float16, (M, N), dev, "dY")
     w = _layer_args(packed, scales, zeros, N, K, group, dev, "")
     if (dY2 is None) != (weights2 is None):
@@ -852,6 +863,8 @@ def w4_gemm_dx_gated(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
     if other is not None:
         with other:
             return w4_gemm_dx_gated(dY, packed, scales, zeros, G, U, activation, group, out, workspace)
+    for c in (activation, group):
+        _code(c, "w4_gemm_dx_gated")
     yp = _arg(dY, torch.float16, (M, N), dev, "dY")
     w = _layer_args(packed, scales, zeros, N, K, group, dev, "")
     gp = _arg(G, torch.float16, (M, K), dev, "G")
@@ -887,6 +900,7 @@ def w4_act_backward(dY: torch.Tensor, Z: torch.Tensor | None, U: torch.Tensor | 
     if other is not None:
         with other:
             return w4_act_backward(dY, Z, U, activation, bias_grad, out, workspace)
+    _code(activation, "w4_act_backward")
     yp = _arg(dY, torch.float16, (M, N), dev, "dY")
     zp = _arg(Z, torch.float16, (M, N), dev, "Z") if Z is not None else None
     up = _arg(U, torch.float16, (M, N), dev, "U") if U is not None else None
