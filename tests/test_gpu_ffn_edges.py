@@ -71,3 +71,28 @@ def test_codes_beyond_an_int_are_refused(value):
                 call(**k)
     assert torch.equal(B.w4_gemm_fused(x, *w, save_pre=2 ** 70)[1], B.w4_gemm_fused(x, *w))  # a truth value
     ok()
+
+
+def test_null_stream_handle_is_the_default_stream():
+    """A raw handle of 0 is the legacy default stream, as at the C entry points: the calls run behind the work
+    queued there, and before the work queued after them."""
+    N, K = 16, 128
+    w = zero_layer(N, K)
+    w[0].fill_(0x11111111)  # W = 1
+    long = ones(4096, 4096) / 4096
+    calls = [lambda x, y: B.w4_gemm_fused(x, *w, stream=0), lambda x, y: B.w4_gemm_gated(x, w, w, activation=B.ACT_NONE, stream=0),
+             lambda x, y: B.w4_gemm_dx(y, *w, stream=0), lambda x, y: B.w4_gemm_dx_gated(y, *w, x, x, activation=B.ACT_NONE, stream=0)[0],
+             lambda x, y: B.w4_act_backward(y, y, activation=B.ACT_NONE, stream=0), lambda x, y: B.w4_gemm(x, *w, stream=0)]
+    for call, want in zip(calls, (1.5 * K, 2.25 * K * K, 1.5 * N, 2.25 * N, 1.5, 1.5 * K)):
+        x, y = ones(2, K), ones(2, N)
+        torch.cuda.synchronize()
+        for _ in range(8):
+            torch.mm(long, long)
+        x.fill_(1.5)
+        y.fill_(1.5)
+        got = call(x, y)
+        x.fill_(1)
+        y.fill_(1)
+        torch.cuda.synchronize()
+        assert bool((got == want).all())
+    ok()

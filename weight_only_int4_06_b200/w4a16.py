@@ -108,6 +108,14 @@ def _stream(stream):
     return ctypes.c_void_p(stream)
 
 
+def _torch_stream(stream, dev) -> torch.cuda.Stream:
+    """torch's object for a stream argument.  The raw handle 0 is the default stream (ExternalStream(0)
+    would be a new one from torch's pool)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+
+
 def _dev(t: torch.Tensor, dtype, name):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -165,12 +173,7 @@ def w4_gemm(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: 
     dev = packed.device
     M, K = X.shape
     N = packed.shape[0]
-    if stream is None:
-        tstream = torch.cuda.current_stream(dev)
-    elif isinstance(stream, torch.cuda.Stream):
-        tstream = stream
-    else:
-        tstream = torch.cuda.ExternalStream(stream, device=dev)
+    tstream = torch.cuda.current_stream(dev) if stream is None else _torch_stream(stream, dev)
     host_out = out is not None and not out.is_cuda
     if host_out and (not host or not out.is_pinned()):
         raise ValueError("a host `out` must be pinned and needs a host X")
@@ -662,8 +665,7 @@ def _other_context(dev, stream):
     workspaces belong to `stream`."""
     if stream is None:
         return None if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream, device=dev)
+    stream = _torch_stream(stream, dev)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
     return torch.cuda.stream(stream)
