@@ -144,8 +144,9 @@ w4_status w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int group, siz
  * slice order by a second launch); skinny for the other M <= 16; TC above 16 rows, with K cut
  * into slices when its tiles fill fewer than half the SMs, or its last wave's tiles when that wave
  * is at most half full, the partials summed in slice order by a further launch):
- *   - GEMV: tensor-core sums of x with the raw operands 1024+q / 1024+16q, offsets and z removed
- *     per group with fp32 activation sums (fixed order), times s16 in fp32;
+ *   - GEMV: tensor-core sums of x with raw operands (1024+q and q-1039, 1024+16q and 16q-1264 with
+ *     fp16(x/16)), offsets and z removed per group with fp32 activation sums (fixed order), times s16
+ *     in fp32; a row with an infinite activation is NaN (the offsets' infinities meet);
  *   - skinny: sum_k x_k (q_k - z) exactly per group on tensor cores in fp32, times s16 in fp32;
  *   - TC: each dequantised weight rounded once to fp16 before the fp32-accumulating MMA.
  * All accumulate in fp32, round Y once to fp16 and are deterministic (fixed reduction orders).
@@ -532,7 +533,9 @@ w4_status w4_gemm_fused_workspace_size(int64_t M, int64_t N, int64_t K, int grou
  *   flags: 0 or W4_FLAG_WEIGHTS_STATIC (see w4_variant; covers packed, scales and zeros).
  *   M <= 8 goes through w4_gemm's GEMV where one launch serves the shape and scales and zeros are
  *   16-byte aligned; it stages half of the activations as fp16(x / 16), which moves an |x| below
- *   2^-10 by up to 2^-21.  Everything else is summed exactly as stored: per group of 128 the products
+ *   2^-10 by up to 2^-21, and sums operands with offsets that cancel over a group: in 2-norm up to
+ *   6e-5 of the products' own, beside the 2e-4 of the output's rounding; a row with an infinite
+ *   activation is NaN.  Everything else is summed exactly as stored: per group of 128 the products
  *   x (q - z) in fp32 on the tensor cores, times s in fp32.
  *   Backward pass: w4_act_backward (dZ, dbias; skip it without activation and bias), w4_gemm_dx;
  *   the residual's gradient is dY.
