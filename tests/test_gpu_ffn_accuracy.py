@@ -11,7 +11,9 @@ most 1.04 sqrt(R^2 + (p |Z|)^2).
     sqrt(sum_i (2^-23 1024 sqrt(16 i) r)^2 / 3) = 1.7e-3 r, against a group's own 2.9 sqrt(128) r = 33 r: 5.2e-5,
     and the same for the sum of all groups, whose errors have no common sign.  p = 2^-14.  fp16(x / 16)
     moves |x| < 2^-10 only (2^-21): nothing beside it.  With offsets of one sign, rows of one sign are off by
-    1e-3 to 3e-3."""
+    1e-3 to 3e-3.
+  * tensor-core products: p = 2^-17 (eight steps of a group's fp32 sum, 2^-22 of it each at most, and the
+    groups' sums).  Weights rounded to fp16 would cost 1.5e-4 = 2^-12.7."""
 import numpy as np
 import pytest
 import torch
@@ -23,7 +25,7 @@ from weight_only_int4_06_b200 import w4a16 as B
 
 pytestmark = pytest.mark.gpu
 
-GEMV = 2.0 ** -14
+GEMV, TC = 2.0 ** -14, 2.0 ** -17
 
 
 def dev(a):
@@ -79,4 +81,31 @@ def test_few_rows(N, K, kind):
         check(B.w4_gemm(Xd, *a), Gr, GEMV, "w4_gemm " + what)
     X = rows(kind, 16, K)
     check(B.w4_gemm(dev(X), *a), X.astype(np.float64) @ Wa.T, GEMV, f"w4_gemm {kind} 16x{N}x{K}")
+    ok()
+
+
+@pytest.mark.parametrize("kind", ["normal", "relu", "negative", "shifted", "loud"])
+@pytest.mark.parametrize("M,N,K", [(9, 2048, 4096), (24, 1032, 11008), (33, 4104, 2176), (64, 2048, 8192), (100, 520, 1152)])
+def test_small_batches(M, N, K, kind):
+    a, Wa = layer(43, N, K)
+    b, Wb = layer(44, N, K)
+    X = rows(kind, M, K)
+    Xd, X64 = dev(X), X.astype(np.float64)
+    Gr, Ur = X64 @ Wa.T, X64 @ Wb.T
+    what = f"{kind} {M}x{N}x{K}"
+    Y, Z = B.w4_gemm_fused(Xd, *a, activation=B.ACT_RELU, save_pre=True)
+    check(Z, Gr, TC, "fused " + what)
+    _, G, U = B.w4_gemm_gated(Xd, a, b, save_pre=True)
+    check(G, Gr, TC, "gate " + what)
+    check(U, Ur, TC, "up " + what)
+    ok()
+
+
+def test_metadata_without_alignment_takes_the_tensor_cores():
+    M, N, K = 4, 2048, 4096
+    (p, s, z), W = layer(45, N, K)
+    s1 = torch.empty(s.numel() + 1, dtype=torch.float16, device="cuda")[1:].view_as(s).copy_(s)
+    z1 = torch.empty(z.numel() + 3, dtype=torch.uint8, device="cuda")[3:].view_as(z).copy_(z)
+    X = rows("relu", M, K)
+    check(B.w4_gemm_fused(dev(X), p, s1, z1), X.astype(np.float64) @ W.T, TC, "misaligned metadata")
     ok()
