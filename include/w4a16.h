@@ -32,8 +32,9 @@
  *                          to read with cudaGetLastError)
  *    Device-side conditions cannot be seen at launch time; kernels record them in a per-device
  *    status word that w4_check_device_status reads:
- *      W4_ERR_RANGE        a group's fp16 scale overflowed (|W * act_scale| too large for fp16);
- *                          the outputs of that call are unspecified
+ *      W4_ERR_RANGE        a group's fp16 scale overflowed (|W * act_scale| too large for fp16), or
+ *                          w4_gemm_dx / w4_gemm_dx_gated met a group whose weights may not fit
+ *                          fp16; the outputs of that call are unspecified
  *      W4_ERR_DEVICE_TIMEOUT  a bounded wait inside a kernel gave up; that kernel's outputs are
  *                          unspecified and the context stays usable
  *      W4_ERR_NUMERIC      gptq_quantize: the damped Hessian is not positive definite (a zero
@@ -576,7 +577,8 @@ w4_status w4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int n_layer
  *   dY, dY2 [M, N] fp16; W, W2 [N, K] (quantised along K as everywhere); dX [M, K] fp16 out.  One
  *   layer: dY2, packed2, scales2 and zeros2 all NULL; two layers: none of them.  The contraction runs
  *   across the groups' scales, so each weight (q - z) s is rounded once to fp16 before the
- *   fp32-accumulating tensor-core product.
+ *   fp32-accumulating tensor-core product.  A group with max(z, 15 - z) s beyond fp16 (65504) is
+ *   recorded as W4_ERR_RANGE in the device status word; the outputs are then unspecified.
  * Errors: as w4_gemm; W4_ERR_NULL when the second layer is given in part.
  */
 w4_status w4_gemm_dx(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const uint32_t* packed,

@@ -96,3 +96,41 @@ def test_null_stream_handle_is_the_default_stream():
         torch.cuda.synchronize()
         assert bool((got == want).all())
     ok()
+
+
+def scaled_layer(N, K, code, zero, scale):
+    """Every weight (code - zero) * scale."""
+    w = zero_layer(N, K)
+    w[0].fill_(int(np.array(code * 0x11111111, np.uint32).view(np.int32)))
+    w[1].fill_(scale)
+    w[2].fill_(zero)
+    return w
+
+
+# the largest weight that a code of the group can have: 15 * 4368 = 65520, 15 * 6000, 8 * 8192 are beyond fp16
+@pytest.mark.parametrize("zero,scale", [(0, 4368.0), (15, 6000.0), (7, 8192.0), (8, 60000.0), (0, float("inf"))])
+def test_weights_beyond_fp16_are_reported(zero, scale):
+    """The input gradients round weights to fp16: a group whose weights may not fit is W4_ERR_RANGE, in any row,
+    group and layer."""
+    N, K, M = 264, 640, 5
+    dY, X = ones(M, N), ones(M, K)
+    good = scaled_layer(N, K, 1, 0, 1.0)
+    for n, g in ((0, 0), (263, 4), (130, 3)):
+        bad = [t.clone() for t in good]
+        bad[1][n, g], bad[2][n, g] = scale, zero
+        for call in (lambda: B.w4_gemm_dx(dY, *bad), lambda: B.w4_gemm_dx(dY, *good, dY2=dY, weights2=tuple(bad)),
+                     lambda: B.w4_gemm_dx_gated(dY, *bad, X, X)):
+            ok()
+            call()
+            assert B.STATUS_NAMES[B.w4_check_device_status()] == "W4_ERR_RANGE"
+    ok()
+
+
+@pytest.mark.parametrize("code,zero,scale", [(15, 0, 4364.0), (0, 15, 4364.0), (15, 7, 8184.0), (0, 8, 8184.0)])
+def test_the_largest_weights_of_fp16_are_right(code, zero, scale):
+    N, K, M = 264, 640, 5
+    w, dY = scaled_layer(N, K, code, zero, scale), ones(M, N) / 4096
+    want = (code - zero) * scale * N / 4096  # the weight rounds to fp16 (2^-11), the output too
+    for got in (B.w4_gemm_dx(dY, *w), B.w4_gemm_dx_gated(dY, *w, ones(M, K), ones(M, K), activation=B.ACT_NONE)[0]):
+        assert bool(((got.double() - want).abs() <= abs(want) * (2.0 ** -10 + 2.0 ** -20)).all())
+    ok()

@@ -4,7 +4,8 @@
 //
 // The contraction runs over the weight's rows, so a group's scale changes along it and cannot be
 // applied to sums: each weight (q - z) s is rounded once to fp16 (2^-11 at most, 1.5e-4 in 2-norm)
-// before the fp32-accumulating product.
+// before the fp32-accumulating product.  A group whose weights may be beyond fp16 (scale 4368 or more, near
+// the limit of fp16 weights) is recorded as W4_ERR_RANGE: an infinite weight would make NaN of zero gradients.
 //
 // One cluster of two CTAs computes 256 columns k of dX by `tn` (32 ... 256) of its rows m: each CTA
 // dequantises its own 128 k (exactly one group: one scale and zero point per weight row) into shared
@@ -95,6 +96,14 @@ __device__ __forceinline__ void dx_finish(const float (&d)[4], int64_t o, uint2 
         *reinterpret_cast<uint2*>(out + o) = half4(dg);
         *reinterpret_cast<uint2*>(out2 + o) = half4(du);
     }
+}
+
+// The smallest fp16 scale (4368) whose largest weight, 15 s, is beyond fp16.
+constexpr uint32_t kLargeScale = 0x6C44u;
+// Whether a code of this group can have a weight (q - z) s beyond fp16.
+__device__ __forceinline__ bool dx_overflows(uint32_t scale, uint32_t z) {
+    const __half s = __ushort_as_half((unsigned short)(scale & 0x7FFFu));
+    return !(__hmul(s, __int2half_rn(max((int)z, 15 - (int)z))) <= __ushort_as_half((unsigned short)0x7BFFu));
 }
 
 // dispatch_act with -1 for "no gate".
@@ -244,6 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
             if (n < p.N && g < G) {
                 sc = __ldg(p.s[second ? 1 : 0] + n * G + g);
                 z = __ldg(p.z[second ? 1 : 0] + n * G + g);
+                if ((sc & 0x7FFFu) >= kLargeScale && dx_overflows(sc, z)) record_status(p.status, W4_ERR_RANGE);
             }
         };
         for (int u = cluster; u < p.units; u += n_clusters) {
