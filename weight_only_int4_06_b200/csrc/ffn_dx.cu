@@ -297,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DX_THREADS, 1)
                                                   (((ch & 7) ^ ((uint32_t)r & 7)) << 4)) = o;
                     }
                 }
-                fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor cores
+                fence_proxy_async_shared();  // the stores are in place for the tensor cores: before the arrival (mbar_arrive_cluster)
                 __syncwarp();
                 if (ok && lane == 0) mbar_arrive_cluster(remote);
                 sc = scn;

@@ -561,7 +561,7 @@ __global__ void __cluster_dims__(FgCfg<NMAX>::kCtas, 1, 1) __launch_bounds__(FgC
                     }
                 }
                 if constexpr (C::kWide) {
-                    fence_proxy_async_shared();  // generic-proxy writes -> visible to the tensor cores
+                    fence_proxy_async_shared();  // the stores are in place for the tensor cores: before the arrival (mbar_arrive_cluster)
                 } else if (ok) {
                     tmem_wait_st();
                     tc_fence_before();

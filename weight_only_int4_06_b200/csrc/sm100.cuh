@@ -260,9 +260,18 @@ __device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank) {
     return r;
 }
 
-// Arrive on an mbarrier of either CTA (address from map_shared).  What the arrival hands over lies in
-// tensor memory or was written by TMA (ordered by tcgen05 fences and the barriers' own phases), so no
-// cluster-scope fence of generic memory goes with it: that would flush and invalidate L1 every time.
+// Arrive on an mbarrier of either CTA (address from map_shared), with the default scope.  What it hands over
+// is read or overwritten by the pair's tensor cores alone, and is in place before the arrival:
+//   - operands that threads stored in their own CTA's shared memory: every storing thread runs
+//     fence_proxy_async_shared() behind its stores, then the warp meets (__syncwarp), then one lane arrives.
+//     Shared memory has one copy, and the fence ends when the stores are in it for the async proxy, through
+//     which the tensor cores read.  Without the fence, or with it before the last store or behind the
+//     arrival, the product that the other CTA issues may read old weights;
+//   - tensor memory that threads have read: tcgen05.wait::ld, then tc_fence_before(), then the arrival.
+// It orders nothing else: for plain loads in the other CTA an arrival has to release at cluster scope.  That
+// drains global memory as well: 300 cycles more on a quiet SM, and with it, or with the fence for
+// shared::cluster, the forward and input-gradient products took a quarter to a third longer (M = 2048, K =
+// 4096, N = 11008: gated 347 us, 460 and 425; pair of input gradients 335, 438 and 436).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
