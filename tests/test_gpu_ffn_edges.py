@@ -134,3 +134,17 @@ def test_the_largest_weights_of_fp16_are_right(code, zero, scale):
     for got in (B.w4_gemm_dx(dY, *w), B.w4_gemm_dx_gated(dY, *w, ones(M, K), ones(M, K), activation=B.ACT_NONE)[0]):
         assert bool(((got.double() - want).abs() <= abs(want) * (2.0 ** -10 + 2.0 ** -20)).all())
     ok()
+
+
+def test_identity_gate_has_derivative_one_everywhere():
+    """Without an activation dG = dH U whatever G holds, as dZ = dY whatever Z holds."""
+    M, N, K = 3, 264, 640
+    w, dY, U = scaled_layer(N, K, 9, 8, 0.25), ones(M, N), ones(M, K) * 3
+    G = ones(M, K)
+    G[1, 5], G[2, 7], G[0, 9] = float("nan"), float("inf"), -float("inf")
+    dG, dU = B.w4_gemm_dx_gated(dY, *w, G, U, activation=B.ACT_NONE)
+    assert bool((dG == 3 * N / 4).all())
+    assert torch.equal(torch.isnan(dU), torch.isnan(G)) and bool((dU[torch.isfinite(G)] == N / 4).all())
+    dG, dU = B.w4_act_backward(U, G, U=U, activation=B.ACT_NONE)
+    assert bool((dG == 9).all()) and torch.equal(torch.isnan(dU), torch.isnan(G))
+    ok()

@@ -190,3 +190,22 @@ def test_input_gradient_through_the_gate(M, N, K, act):
     what = f"dx_gated {M}x{N}x{K} {act}"
     check(dG, rG, e * np.abs(U64 * F.act_grad(G64, act)) + A * np.abs(dH * U64), what + " dG")
     check(dU, rU, e * np.abs(F.act(G64, act)) + A * np.abs(rU), what + " dU")
+
+
+def test_static_weights_chain():
+    """W4_FLAG_WEIGHTS_STATIC: the weights' first stages are fetched before the preceding call has finished."""
+    D, Fi, M = 2048, 5504, 600
+    g, u, d = (layer(82 + i, *s)[1] for i, s in enumerate(((Fi, D), (Fi, D), (D, Fi))))
+    X = dev(synth.layer_case(82, M, D, 8)[0])
+
+    def chain(flags):
+        x = X
+        for _ in range(3):
+            x = B.w4_gemm_fused(B.w4_gemm_gated(X, g, u, flags=flags), *d, residual=x, flags=flags)
+        return x
+
+    plain = chain(0)
+    assert bool(torch.isfinite(plain).all())
+    for _ in range(4):
+        assert torch.equal(plain, chain(B.FLAG_WEIGHTS_STATIC))
+    ok()
