@@ -85,6 +85,17 @@ def test_few_rows(N, K, kind):
 
 
 @pytest.mark.parametrize("kind", ["normal", "relu", "negative", "shifted", "loud"])
+@pytest.mark.parametrize("N,K", [(4096, 4096), (2048, 1152)])
+def test_gemv_with_weights_in_tensor_memory(N, K, kind):
+    """The same operands in w4_gemm's other GEMV."""
+    a, Wa = layer(41, N, K)
+    for M in (1, 8):
+        X = rows(kind, M, K)
+        check(B.w4_gemm(dev(X), *a, variant=B.VARIANT_GEMV_TC), X.astype(np.float64) @ Wa.T, GEMV, f"{kind} {M}x{N}x{K}")
+    ok()
+
+
+@pytest.mark.parametrize("kind", ["normal", "relu", "negative", "shifted", "loud"])
 @pytest.mark.parametrize("M,N,K", [(9, 2048, 4096), (24, 1032, 11008), (33, 4104, 2176), (64, 2048, 8192), (100, 520, 1152)])
 def test_small_batches(M, N, K, kind):
     a, Wa = layer(43, N, K)

@@ -21,20 +21,12 @@
 //    writes Y waits for it.
 //  * Sixteen consumer warps; warp w takes the two consecutive groups 2w, 2w + 1 of every stage
 //    and runs mma.sync m16n8k16 with the 16 weight rows as the A operand and the (up to 8)
-//    activation rows as B.  Dequantisation is one LOP3 per two weights, the raw fp16 values of a nibble
-//    under an exponent, with opposite signs in the two halves of a register:
-//        low nibble of a byte    1024 + q    and  -(1024 + 15 - q)        = q - 1039
-//        high nibble             1024 + 16 q and  -(1024 + 16 (15 - q))   = 16 q - 1264
-//    Activations that meet high nibbles are staged pre-multiplied by 1/16, and the constant offsets and the
-//    zero point are removed per group in fp32 with the activation sums
-//        sum_k x_k (q_k - z) = raw - C - z S,  S = sum_k x_k,
-//        C = 1024 (Sl0 + Sh0') - 1039 Sl1 - 1264 Sh1',
-//    Sl the sums of x over low-nibble slots, Sh' of the staged x/16 over high-nibble slots, of the lower and
-//    upper halves, in fp32 in a fixed tree order (deterministic).  The group's fp16 scale then multiplies
-//    that difference in fp32.  Why opposite signs: the MMA's fp32 sums are cut off towards zero, so with
-//    offsets of one sign every partial sum of a row of one-signed activations (behind a relu, say) lost half
-//    a step of 2^17 in the same direction: all outputs off by 1.2e-3 (K = 4096) to 3.1e-3 (K = 28672) of
-//    their rms.  With both signs the offsets cancel as they are summed, whatever the activations' mean.
+//    activation rows as B.  Dequantisation is one LOP3 per two weights: the operands are raw fp16 values
+//    with offsets of both signs (raw_low, raw_high in common.cuh); activations that meet high nibbles
+//    are staged pre-multiplied by 1/16, and the offsets C and the zero point are removed per group in fp32
+//    with the activation sums (raw_offsets, added in a fixed tree order: deterministic)
+//        sum_k x_k (q_k - z) = raw - C - z S.
+//    The group's fp16 scale then multiplies that difference in fp32.
 //  * Each consumer warp stages only the activations of its own groups, each 8-k chunk as
 //    [x0, x4, x1/16, x5/16, x2, x6, x3/16, x7/16] so that one 16-byte shared load yields the B
 //    fragments of the two MMAs that consume one packed word; no CTA-wide barrier stands between
@@ -106,9 +98,6 @@ __host__ __device__ inline DsLayout ds_layout(int SG, int MT, int M, int K, int 
 // makes the B-fragment loads of a warp bank-conflict free for up to 8 activation rows.
 __device__ __forceinline__ int ds_swz(int ch) { return ch ^ ((ch >> 2) & 2); }
 
-// The two fp16 halves of a packed pair, in fp32.
-__device__ __forceinline__ float2 half2_floats(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
-
 constexpr int DS_XILP = 4;  // activation chunks each consumer thread loads before using any
 
 // Shared-memory loads through 32-bit shared addresses (volatile: they stay behind the mbarrier waits).
@@ -143,10 +132,6 @@ __device__ __forceinline__ float ds_half(uint32_t v, int h) {
     return __half2float(__ushort_as_half((unsigned short)(h ? (v >> 16) : (v & 0xFFFFu))));
 }
 
-// The low or high nibbles of bytes 0 and 2 of a word as raw fp16 operands (file header).
-__device__ __forceinline__ uint32_t ds_low(uint32_t w) { return lop3_and_xor(w, 0x000F000Fu, 0xE40F6400u); }
-__device__ __forceinline__ uint32_t ds_high(uint32_t w) { return lop3_and_xor(w, 0x00F000F0u, 0xE4F06400u); }
-
 // One group (16 rows x 128 k) for this thread: raw tensor-core sums, then the offsets and the zero
 // point removed with the group's activation sums and the scale applied, into acc.
 template <int MT>
@@ -163,8 +148,8 @@ __device__ __forceinline__ void ds_group(uint32_t a_addr, uint32_t b_addr, uint3
         const uint32_t a = wA[j], b = wB[j], a8 = a >> 8, b8 = b >> 8;
         const uint4 xf = xlane ? lds128(xg + xofs[j]) : make_uint4(0u, 0u, 0u, 0u);
         float(&cc)[4] = (j & 1) ? c1 : c0;  // two independent accumulation chains
-        mma_16816(cc, ds_low(a), ds_low(b), ds_high(a), ds_high(b), xf.x, xf.y);
-        mma_16816(cc, ds_low(a8), ds_low(b8), ds_high(a8), ds_high(b8), xf.z, xf.w);
+        mma_16816(cc, raw_low(a), raw_low(b), raw_high(a), raw_high(b), xf.x, xf.y);
+        mma_16816(cc, raw_low(a8), raw_low(b8), raw_high(a8), raw_high(b8), xf.z, xf.w);
     }
     // rows g8 + 8 of a half tile (N % 16 == 8) hold stale metadata; never stored
     if (MT == 1) {
@@ -204,13 +189,13 @@ __device__ __forceinline__ void ds_group16(uint32_t a_addr, uint32_t b_addr, uin
         const uint32_t a = wA[j], b = wB[j], a8 = a >> 8, b8 = b >> 8;
         const uint4 xf0 = x0 ? lds128(xg0 + xofs[j]) : make_uint4(0u, 0u, 0u, 0u);
         const uint4 xf1 = x1 ? lds128(xg1 + xofs[j]) : make_uint4(0u, 0u, 0u, 0u);
-        uint32_t f0 = ds_low(a), f1 = ds_low(b), f2 = ds_high(a), f3 = ds_high(b);
+        uint32_t f0 = raw_low(a), f1 = raw_low(b), f2 = raw_high(a), f3 = raw_high(b);
         mma_16816(c0, f0, f1, f2, f3, xf0.x, xf0.y);
         mma_16816(c1, f0, f1, f2, f3, xf1.x, xf1.y);
-        f0 = ds_low(a8);
-        f1 = ds_low(b8);
-        f2 = ds_high(a8);
-        f3 = ds_high(b8);
+        f0 = raw_low(a8);
+        f1 = raw_low(b8);
+        f2 = raw_high(a8);
+        f3 = raw_high(b8);
         mma_16816(c0, f0, f1, f2, f3, xf0.z, xf0.w);
         mma_16816(c1, f0, f1, f2, f3, xf1.z, xf1.w);
     }
@@ -500,10 +485,8 @@ __global__ void __launch_bounds__(DS_THREADS, 1)
                 hh = __hmul2(*reinterpret_cast<__half2*>(&h), sixteenth);
                 p.w = *reinterpret_cast<uint32_t*>(&hh);
                 *reinterpret_cast<uint4*>(xs + (int64_t)m * RS + ds_swz(ch) * 8) = p;
-                const float2 l0 = half2_floats(p.x), l1 = half2_floats(p.z), h0 = half2_floats(p.y), h1 = half2_floats(p.w);
-                const float la = l0.x + l1.x, lb = l0.y + l1.y, ha = h0.x + h1.x, hb = h0.y + h1.y;
-                float C = fmaf(-1264.0f, hb, fmaf(-1039.0f, lb, 1024.0f * (la + ha)));
-                float S = fmaf(16.0f, ha + hb, la + lb);
+                float C, S;
+                raw_offsets(p, C, S);
 #pragma unroll
                 for (int o = 8; o; o >>= 1) {
                     C += __shfl_xor_sync(half_mask, C, o);

@@ -7,16 +7,14 @@
 // At HBM rate a B200 SM must consume ~46 weights per cycle, so the per-weight work on the CUDA
 // cores has to be minimal.  Here it is one LOP3 per two weights plus a TMEM store per 64:
 //  * the 128 weight rows of a tile are the MMA's A operand and live in TMEM: each dequant thread
-//    owns one row (one TMEM lane), turns 8 codes into four f16x2 registers holding the raw values
-//    1024+q (low nibble of a byte) and 1024+16q (high nibble) with one LOP3 per register, and
-//    stores 64 of them with one tcgen05.st;
+//    owns one row (one TMEM lane), turns 8 codes into four f16x2 registers of raw values with one LOP3
+//    each (raw_low, raw_high in common.cuh), and stores 64 of them with one tcgen05.st;
 //  * one thread issues tcgen05.mma (M=128, N=16, K=16, A from TMEM, activations as B from shared
 //    memory, fp32 accumulator in TMEM), one 128 x 16 accumulator per group of 128 k;
 //  * the activations are staged once with every 8-k chunk in the slot order of those registers,
-//    [x0, x4, x1/16, x5/16, x2, x6, x3/16, x7/16] (rows beyond M are zero), and the exact sums
-//    Sl (low-nibble slots) and Sh' (staged x/16) of each group remove the operand offsets and
-//    the zero point:  sum_k x_k (q_k - z) = raw - 1024 (Sl + Sh') - z (Sl + 16 Sh');
-//    the group's fp16 scale then multiplies that exact-as-fp32 sum, accumulated in fp32;
+//    [x0, x4, x1/16, x5/16, x2, x6, x3/16, x7/16] (rows beyond M are zero), and each group's sums of
+//    them remove the operands' offsets and the zero point:  sum_k x_k (q_k - z) = raw - C - z S
+//    (raw_offsets); the group's fp16 scale then multiplies that difference, accumulated in fp32;
 //  * the weights stream through a 3-stage TMA ring (128 rows x 256 k, 128-byte swizzle);
 //  * a CTA owns 128 rows and one K split; the splits of a row tile form a thread-block cluster
 //    and their partial sums are added in split order through distributed shared memory.
@@ -58,11 +56,6 @@ __host__ __device__ inline GtLayout gt_layout(int gps) {
     L.bars = L.part + 2 * GT_ROWS * GT_MAXM * 4;    // [parity][row][m] fp32
     L.total = L.bars + 8 * (2 * GT_WSTAGES + 2 * GT_NA + 2 * GT_ND) + 16;
     return L;
-}
-
-__device__ __forceinline__ float gt_half2_sum(uint32_t h) {  // sum of the two halves, in fp32
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return f.x + f.y;
 }
 
 __device__ __forceinline__ void gt_deq_barrier() {
@@ -223,15 +216,14 @@ __global__ void __launch_bounds__(GT_THREADS, 2)
                 hh = __hmul2(*reinterpret_cast<__half2*>(&t), sixteenth);
                 p.w = *reinterpret_cast<uint32_t*>(&hh);
                 *reinterpret_cast<uint4*>(smem + L.xs + ch * 256 + m * 16) = p;  // m < 8
-                float lo = gt_half2_sum(p.x) + gt_half2_sum(p.z);
-                float hi = gt_half2_sum(p.y) + gt_half2_sum(p.w);
+                float C, S;
+                raw_offsets(p, C, S);
 #pragma unroll
                 for (int o = 8; o; o >>= 1) {
-                    lo += __shfl_xor_sync(half_mask, lo, o);
-                    hi += __shfl_xor_sync(half_mask, hi, o);
+                    C += __shfl_xor_sync(half_mask, C, o);
+                    S += __shfl_xor_sync(half_mask, S, o);
                 }
-                if ((ch & 15) == 0)  // C = 1024 (Sl + Sh'), S = Sl + 16 Sh'
-                    corr[(ch >> 4) * GT_MAXM + m] = make_float2(1024.0f * (lo + hi), fmaf(16.0f, hi, lo));
+                if ((ch & 15) == 0) corr[(ch >> 4) * GT_MAXM + m] = make_float2(C, S);
             }
         }
         fence_proxy_async_shared();  // staged activations: generic-proxy writes read by the MMA
@@ -290,10 +282,10 @@ __global__ void __launch_bounds__(GT_THREADS, 2)
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t w = wd[j], w8 = w >> 8;
                         uint32_t* o = regs + (cc * 4 + j) * 4;
-                        o[0] = lop3_and_or(w, 0x000F000Fu, 0x64006400u);   // 1024 + n0, 1024 + n4
-                        o[1] = lop3_and_or(w, 0x00F000F0u, 0x64006400u);   // 1024 + 16 n1, 1024 + 16 n5
-                        o[2] = lop3_and_or(w8, 0x000F000Fu, 0x64006400u);  // 1024 + n2, 1024 + n6
-                        o[3] = lop3_and_or(w8, 0x00F000F0u, 0x64006400u);  // 1024 + 16 n3, 1024 + 16 n7
+                        o[0] = raw_low(w);    // k0, k4
+                        o[1] = raw_high(w);   // k1, k5
+                        o[2] = raw_low(w8);   // k2, k6
+                        o[3] = raw_high(w8);  // k3, k7
                     }
                 }
                 tmem_st_32x32b_x32(tmem + lane_base + a * 64 + half * 32, regs);
