@@ -534,8 +534,8 @@ w4_status w4_gemm_fused_workspace_size(int64_t M, int64_t N, int64_t K, int grou
  *   flags: 0 or W4_FLAG_WEIGHTS_STATIC (see w4_variant; covers packed, scales and zeros).
  *   M <= 8 goes through w4_gemm's GEMV where one launch serves the shape and scales and zeros are
  *   16-byte aligned; it stages half of the activations as fp16(x / 16), which moves an |x| below
- *   2^-10 by up to 2^-21, and sums operands with offsets that cancel over a group: in 2-norm up to
- *   6e-5 of the products' own, beside the 2e-4 of the output's rounding; a row with an infinite
+ *   2^-10 by up to 2^-21, and sums operands with offsets that cancel over a group: in 2-norm below
+ *   1e-4 of the products, beside the 2e-4 of the output's rounding; a row with an infinite
  *   activation is NaN.  Everything else is summed exactly as stored: per group of 128 the products
  *   x (q - z) in fp32 on the tensor cores, times s in fp32.
  *   Backward pass: w4_act_backward (dZ, dbias; skip it without activation and bias), w4_gemm_dx;

@@ -10,7 +10,7 @@
 //
 // The normal distribution function's tail is Phi(-|x|) = Q(t) exp(-x^2 / 2), t = 1 / (1 + P |x|), Q a
 // polynomial fitted here (iteratively reweighted least squares of the relative error on |x| <= 14:
-// at most 6.4e-7); the derivative needs the same exponential.
+// at most 7.2e-7); the derivative needs the same exponential.
 #pragma once
 
 #include "common.cuh"

@@ -14,7 +14,8 @@
 // in and out 64 KB, codes in and out 16 KB, weights in and out 64 KB: 144 KB in the 1024 cycles of the
 // products, 1.1 times what its port moves; that bounds the kernel (the forward product's way, weights
 // through tensor memory, needs lanes of k, and eight lanes would share every packed word).
-// M = 2048, K = 4096, N = 11008, both layers: 289 us (1277 TFLOP/s).
+// M = 2048, K = 4096, N = 11008, both layers: 289 us (1277 TFLOP/s) in a short burst, 340 us (1090) called
+// without a pause, where the power limit holds the clock down.
 //
 //   warp 0       TMA producer: per 128 n the dY tile (two boxes of 64 n) and 128 packed rows of 64 bytes
 //   warp 1       CTA 0: issues the pair's tcgen05.mma (M = 256, N = tn, K = 16)

@@ -20,7 +20,8 @@
 //             two groups a step.  Bound by the dequantisation (a step's codes come in, are converted and
 //             stored to tensor memory; two steps in flight): 780 cycles a group, in 340 of which the ALU pipe
 //             converts, where HBM would allow 370; 48 us at M = 32, K = 28672, N = 8192.
-// At M = 2048, K = 4096, N = 11008: gated 289 us (1280 TFLOP/s), plain 145 us.
+// At M = 2048, K = 4096, N = 11008, in a short burst: gated 289 us (1280 TFLOP/s), plain 145 us; called without
+// a pause, where the power limit holds the clock down, gated 347 us (1065 TFLOP/s).
 //
 //   warp 0       TMA producer of its CTA: X (boxes of 64 k) and the packed rows of a step
 //   warp 1       first CTA: issues the tcgen05.mma (N = tn, K = 16) and one commit a step
@@ -758,8 +759,11 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
             if (ks > 1 && (tiles * (ks - 1) >= slots || G / ks < 4)) break;
             const int64_t units = tiles * ks;
             const int64_t waves = (units + slots - 1) / slots;
-            // cycles per group (measured: 1152 at tn = 192, 1258 at 256); per unit: filling and the epilogue (33
-            // per column); a second launch and its traffic when K is cut.  Small tiles: 780 a group measured
+            // cycles per group; per unit: filling and the epilogue (33 per column); a second launch and its
+            // traffic when K is cut.  Large tiles: 1258 measured at tn = 256, and the other widths by the line
+            // through it: 0.79, 0.83, 0.87, 0.91, 0.96 of it at tn = 96, 128, 160, 192, 224, where full waves
+            // (M = 8 tn, N = 18944, K = 8192 less 4096) measured 0.80, 0.81, 0.86, 0.88, 0.97 (700, 708, 752, 767,
+            // 844 ns against 871).  Small tiles: 780 a group measured
             // with the start and end of the kernel; 630 chooses best between the two instantiations.  700 gives
             // M = 96, K = N = 4096 to large tiles (23.5 us, 19.5 in small ones) and the gated M = 96, K = 4096, N =
             // 11008 (55, 51); 560 leaves the gated M = 192, K = 4096, N = 11008 to small ones (63, 61 in large).
@@ -779,9 +783,9 @@ FgPlan fg_plan(int64_t M, int64_t N, int64_t K, bool gated) {
         }
         // shares: one for each SM, with a fill and an epilogue for each tile that a share touches, and its
         // first and last tile's partial sums written and read
-        // (M = 32: gated K = 8192, N = 28672 123 us in whole tiles, 103 in shares; gated K = 4096, N = 11008
-        // 39, 34; plain K = 28672, N = 8192 64 in two slices, 60 in shares; where the rule is near its edge
-        // either is up to 2 us better)
+        // (M = 32: gated K = 8192, N = 28672 99.9 us in whole tiles, 89.8 in shares; gated K = 4096, N = 11008
+        // 29.4, 26.2; plain K = 28672, N = 8192 51.4 in two slices, 50.2 in shares; M = 64: gated K = 8192, N =
+        // 28672 107.1, 96.3; where the rule is near its edge either is up to 2 us better)
         const int64_t steps = (G + 1) / 2, total = n_tiles * steps, len = total / sms;
         if (wide || m_tiles > 1 || len < 4 || total * sms >= (1ll << 29)) continue;
         const int64_t longest = (total + sms - 1) / sms, per = (longest + steps - 2) / steps + 1;
