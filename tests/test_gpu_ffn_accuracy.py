@@ -14,6 +14,8 @@ most 1.04 sqrt(R^2 + (p |Z|)^2).
     1e-3 to 3e-3.
   * tensor-core products: p = 2^-17 (eight steps of a group's fp32 sum, 2^-22 of it each at most, and the
     groups' sums).  Weights rounded to fp16 would cost 1.5e-4 = 2^-12.7."""
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -32,6 +34,7 @@ def dev(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
 
+@functools.lru_cache(maxsize=4)
 def layer(case, N, K):
     lay = oracle.quantize_pack(synth.layer_case(case, 1, K, N)[1])
     return tuple(dev(t) for t in (lay[0].view(np.int32), lay[1], lay[2])), F.weight(lay)

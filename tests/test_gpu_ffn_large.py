@@ -18,6 +18,7 @@ Single elements: five standard deviations of those 2-norms' parts, 2^-9 of the r
 gradients (4.6 of 4.2e-4 rms), 2^-14 for the forward products, behind half a step of the output.  What
 follows a product carries its error through its derivatives, at most 1.13 for every activation."""
 import functools
+import math
 
 import numpy as np
 import pytest
@@ -47,35 +48,69 @@ def layer(case, N, K):
 
 
 def normal(seed, M, N, std):
-    return (np.random.default_rng(seed).standard_normal((M, N)) * std).astype(np.float16)
+    """The same values on every run, on the GPU."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    return (torch.randn(M, N, generator=gen, device="cuda") * std).half()
+
+
+# The activations and their derivatives in 64 bits, on the GPU (oracle/ffn_oracle.py has them on the host).
+def act(x, name):
+    if name == "relu":
+        return x.clamp(min=0)
+    if name == "gelu":
+        return x * torch.special.ndtr(x)
+    if name == "gelu_tanh":
+        return 0.5 * x * (1 + torch.tanh(math.sqrt(2 / math.pi) * (x + 0.044715 * x ** 3)))
+    return x * torch.sigmoid(x) if name == "silu" else x
+
+
+def act_grad(x, name):
+    if name == "relu":
+        return (x > 0).double()
+    if name == "gelu":
+        return torch.special.ndtr(x) + x * torch.exp(-0.5 * x * x) / math.sqrt(2 * math.pi)
+    if name == "gelu_tanh":
+        c = math.sqrt(2 / math.pi)
+        t = torch.tanh(c * (x + 0.044715 * x ** 3))
+        return 0.5 * (1 + t) + 0.5 * x * (1 - t * t) * c * (1 + 3 * 0.044715 * x * x)
+    if name == "silu":
+        s = torch.sigmoid(x)
+        return s * (1 + x * (1 - s))
+    return torch.ones_like(x)
+
+
+def test_the_formulas_here_are_the_oracles():
+    x = np.linspace(-12, 12, 4001)
+    for name in F.ACTIVATIONS:
+        assert np.allclose(act(dev(x), name).cpu().numpy(), F.act(x, name), rtol=1e-9, atol=1e-13)
+        assert np.allclose(act_grad(dev(x), name).cpu().numpy(), F.act_grad(x, name), rtol=1e-9, atol=1e-12)
 
 
 def rms(a):
-    return float(np.sqrt(np.mean(np.square(a))))
+    return float(a.square().mean().sqrt())
 
 
 def half_step(a):
     """Half an fp16 step at each value of a."""
-    return 0.5 * np.spacing(np.minimum(np.abs(a), 65504.0).astype(np.float16)).astype(np.float64)
+    return torch.exp2(torch.floor(torch.log2(a.abs().clamp(min=2.0 ** -14))) - 11)
 
 
 def check(got, ref, slack, what):
-    got = got.detach().cpu().numpy().astype(np.float64)
     assert got.shape == ref.shape, what
-    assert np.isfinite(got).all(), what
-    err = np.abs(got - ref)
-    bound = HALF * (np.abs(ref) + slack) + 2.0 ** -25 + slack
+    assert bool(torch.isfinite(got).all()), what
+    err = (got.double() - ref).abs()
+    bound = HALF * (ref.abs() + slack) + 2.0 ** -25 + slack
     bad = err > bound
-    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, first {np.argwhere(bad)[:3].tolist()}; worst {np.max(err / bound):.3g} bounds"
-    return got
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} off, first {bad.nonzero()[:3].tolist()}; worst {float((err / bound).max()):.3g} bounds"
 
 
 def check_product(got, ref, norm, each, what):
-    got = check(got, ref, each * rms(ref), what)
-    R = np.sqrt(np.sum(np.square(half_step(ref))) / 3.0)
-    limit = 1.01 * np.sqrt(R * R + (norm * np.linalg.norm(ref)) ** 2)
-    err = np.linalg.norm(got - ref)
-    assert err <= limit, f"{what}: 2-norm {err / np.linalg.norm(ref):.3e}, limit {limit / np.linalg.norm(ref):.3e}"
+    check(got, ref, each * rms(ref), what)
+    size, err = float(ref.norm()), float((got.double() - ref).norm())
+    R = float((half_step(ref).square().sum() / 3).sqrt())
+    limit = 1.01 * math.sqrt(R * R + (norm * size) ** 2)
+    assert err <= limit, f"{what}: 2-norm {err / size:.3e}, limit {limit / size:.3e}"
 
 
 def ok():
@@ -100,43 +135,42 @@ def forward_case(M, N, K, gated):
     Xd = dev(X)
     a = layer(31, N, K)
     b = layer(32, N, K) if gated else None
-    product = lambda lay: (Xd.double() @ lay[2].t()).cpu().numpy()
+    product = lambda lay: Xd.double() @ lay[2].t()
     return Xd, a[1], product(a), b and b[1], b and product(b)
 
 
-@pytest.mark.parametrize("act", F.ACTIVATIONS)
+@pytest.mark.parametrize("name", F.ACTIVATIONS)
 @pytest.mark.parametrize("M,N,K", FORWARD)
-def test_fused(M, N, K, act):
+def test_fused(M, N, K, name):
     Xd, lay, Z0, _, _ = forward_case(M, N, K, False)
-    i = F.ACTIVATIONS.index(act)
+    i = F.ACTIVATIONS.index(name)
     for bias, residual, pre in ((False, False, True), (True, True, i % 2 == 0), (i % 2 == 0, i % 2 == 1, True)):
-        b = normal([31, 1], 1, N, 0.5)[0] if bias else None
-        r = normal([31, 2], M, N, 2.0) if residual else None
-        out = B.w4_gemm_fused(Xd, *lay, bias=None if b is None else dev(b), activation=B.ACTIVATIONS[act],
-                              residual=None if r is None else dev(r), save_pre=pre)
+        b = normal(1, 1, N, 0.5)[0] if bias else None
+        r = normal(2, M, N, 2.0) if residual else None
+        out = B.w4_gemm_fused(Xd, *lay, bias=b, activation=B.ACTIVATIONS[name], residual=r, save_pre=pre)
         ok()
         Y, Z = out if pre else (out, None)
-        Zr = Z0 if b is None else Z0 + b.astype(np.float64)
-        Yr = F.act(Zr, act) if r is None else F.act(Zr, act) + r.astype(np.float64)
-        what = f"fused {M}x{N}x{K} {act} bias={bias} residual={residual}"
+        Zr = Z0 if b is None else Z0 + b.double()
+        Yr = act(Zr, name) if r is None else act(Zr, name) + r.double()
+        what = f"fused {M}x{N}x{K} {name} bias={bias} residual={residual}"
         # the fp32 sum's error, and the activation's and residual's own fp32 arithmetic on values of Z's size
-        check(Y, Yr, (1.13 * FWD_EACH + A) * rms(Zr) + A * np.abs(Zr), what)
+        check(Y, Yr, (1.13 * FWD_EACH + A) * rms(Zr) + A * Zr.abs(), what)
         if pre:
             check_product(Z, Zr, FWD_NORM, FWD_EACH, what + " Z")
 
 
-@pytest.mark.parametrize("act", F.ACTIVATIONS)
+@pytest.mark.parametrize("name", F.ACTIVATIONS)
 @pytest.mark.parametrize("M,N,K", FORWARD)
-def test_gated(M, N, K, act):
+def test_gated(M, N, K, name):
     Xd, g, Gr, u, Ur = forward_case(M, N, K, True)
-    Hr = F.act(Gr, act) * Ur
+    Ga = act(Gr, name)
     eg, eu = FWD_EACH * rms(Gr), FWD_EACH * rms(Ur)
-    slack = 1.13 * eg * (np.abs(Ur) + eu) + eu * np.abs(F.act(Gr, act)) + A * np.abs(Gr * Ur)
-    H, G, U = B.w4_gemm_gated(Xd, g, u, activation=B.ACTIVATIONS[act], save_pre=True)
-    H2 = B.w4_gemm_gated(Xd, g, u, activation=B.ACTIVATIONS[act])
+    slack = 1.13 * eg * (Ur.abs() + eu) + eu * Ga.abs() + A * (Gr * Ur).abs()
+    H, G, U = B.w4_gemm_gated(Xd, g, u, activation=B.ACTIVATIONS[name], save_pre=True)
+    H2 = B.w4_gemm_gated(Xd, g, u, activation=B.ACTIVATIONS[name])
     ok()
-    what = f"gated {M}x{N}x{K} {act}"
-    check(H, Hr, slack, what)
+    what = f"gated {M}x{N}x{K} {name}"
+    check(H, Ga * Ur, slack, what)
     assert torch.equal(H, H2)
     check_product(G, Gr, FWD_NORM, FWD_EACH, what + " G")
     check_product(U, Ur, FWD_NORM, FWD_EACH, what + " U")
@@ -156,13 +190,13 @@ BACKWARD = [
 @functools.lru_cache(maxsize=2)
 def backward_case(M, N, K, pair):
     a = layer(51, N, K)
-    dY = dev(normal([51, 3], M, N, 0.05))
+    dY = normal(3, M, N, 0.05)
     dX = dY.double() @ a[2]
     if not pair:
-        return dY, a[1], dX.cpu().numpy(), None, None
+        return dY, a[1], dX, None, None
     b = layer(52, N, K)
-    dY2 = dev(normal([51, 4], M, N, 0.05))
-    return dY, a[1], (dX + dY2.double() @ b[2]).cpu().numpy(), dY2, b[1]
+    dY2 = normal(4, M, N, 0.05)
+    return dY, a[1], dX + dY2.double() @ b[2], dY2, b[1]
 
 
 @pytest.mark.parametrize("pair", [False, True])
@@ -174,22 +208,21 @@ def test_input_gradient(M, N, K, pair):
     check_product(out, ref, DX_NORM, DX_EACH, f"dx {M}x{N}x{K} pair={pair}")
 
 
-@pytest.mark.parametrize("act", F.ACTIVATIONS)
+@pytest.mark.parametrize("name", F.ACTIVATIONS)
 @pytest.mark.parametrize("M,N,K", BACKWARD)
-def test_input_gradient_through_the_gate(M, N, K, act):
+def test_input_gradient_through_the_gate(M, N, K, name):
     dY, a, dH, _, _ = backward_case(M, N, K, False)
-    G, U = normal([61, 6], M, K, 1.5), normal([61, 7], M, K, 1.5)
-    Gd, Ud = dev(G), dev(U)
-    dG, dU = B.w4_gemm_dx_gated(dY, *a, Gd, Ud, activation=B.ACTIVATIONS[act])
-    in_place = B.w4_gemm_dx_gated(dY, *a, Gd, Ud, activation=B.ACTIVATIONS[act], out=(Gd, Ud))
+    G, U = normal(6, M, K, 1.5), normal(7, M, K, 1.5)
+    G64, U64 = G.double(), U.double()
+    dG, dU = B.w4_gemm_dx_gated(dY, *a, G, U, activation=B.ACTIVATIONS[name])
+    in_place = B.w4_gemm_dx_gated(dY, *a, G, U, activation=B.ACTIVATIONS[name], out=(G, U))
     ok()
-    assert in_place[0] is Gd and torch.equal(dG, Gd) and torch.equal(dU, Ud)
-    rG, rU = F.gate_backward(dH, G, U, act)
+    assert in_place[0] is G and torch.equal(dG, G) and torch.equal(dU, U)
     e = DX_EACH * rms(dH)
-    U64, G64 = U.astype(np.float64), G.astype(np.float64)
-    what = f"dx_gated {M}x{N}x{K} {act}"
-    check(dG, rG, e * np.abs(U64 * F.act_grad(G64, act)) + A * np.abs(dH * U64), what + " dG")
-    check(dU, rU, e * np.abs(F.act(G64, act)) + A * np.abs(rU), what + " dU")
+    what = f"dx_gated {M}x{N}x{K} {name}"
+    check(dG, dH * U64 * act_grad(G64, name), e * (U64 * act_grad(G64, name)).abs() + A * (dH * U64).abs(), what + " dG")
+    rU = dH * act(G64, name)
+    check(dU, rU, e * act(G64, name).abs() + A * rU.abs(), what + " dU")
 
 
 def test_static_weights_chain():
